@@ -483,6 +483,223 @@ bitnet_status bitnet_ternary_matmul_stages(int64_t M, const bitnet_problem *prob
                                            void *workspace, size_t workspace_bytes,
                                            void *stream);
 
+/* ------------------------------------------------------------------------
+ * The paged key-value cache and the decode step around the projections.
+ * The decoder keeps a key-value cache and decodes token by token (ONNX model
+ * card, Layout table, "decoder_model_merged"; blog "The Paper Says ARM
+ * Support...", section "Round three", on logits and tokens).  The pages give
+ * no cache format; these calls are this library's own:
+ *   bitnet_kv_map            pages, slots and positions of a step's tokens
+ *   bitnet_kv_append         rotate q and k, write k and v into the pages
+ *   bitnet_paged_attention   attention of one new token per row
+ *   bitnet_beam_select       the next beams (or greedy tokens) from the logits
+ *   bitnet_beam_reorder      the pages of the selected beams
+ * Lengths, page numbers and parents are DEVICE data that the host never
+ * reads, so a step can be queued, or captured into a graph, without waiting
+ * for the GPU.  Values out of range in them are defined below; none makes a
+ * kernel touch memory outside the buffers it was given.
+ *
+ * The cache: keys and values of `layers` layers in `pages` pages of
+ * page_size tokens, kv_heads heads of head_dim channels.  Element (layer,
+ * page, head, token, channel) of k and of v is at
+ *   layer*layer_stride + page*page_stride + head*head_stride +
+ *   token*token_stride + channel
+ * elements, so heads may come before tokens in memory or after them.
+ * Slot s of the cache is token s % page_size of page s / page_size.
+ *   dtype        BITNET_KV_BF16, BITNET_KV_FP16, or BITNET_KV_INT8: int8 codes
+ *                with one fp32 scale per (layer, page, head, token) in k_scale
+ *                and v_scale [layers][pages][kv_heads][page_size] (contiguous;
+ *                NULL for the other types): value = code * scale,
+ *                scale = fl32(max|x| / 127) of the row, code =
+ *                clamp(rint(fl32(x / scale)), -127, 127); a row of zeros, or
+ *                one whose scale rounds to zero, gives scale 0 and codes 0.
+ *   limits       head_dim 64, 128 or 256; page_size a power of two, 1..1024;
+ *                layers 1..1024, kv_heads 1..256, pages >= 1,
+ *                pages * page_size < 2^31; k and v 16-byte aligned, strides
+ *                multiples of 16 bytes, at least head_dim and below 2^40
+ *                elements (layer_stride is not looked at when layers == 1).
+ * The struct itself is host memory, read during the call.
+ * ------------------------------------------------------------------------ */
+#define BITNET_KV_BF16 0
+#define BITNET_KV_FP16 1
+#define BITNET_KV_INT8 2
+
+typedef struct bitnet_kv_cache {
+    void *k;
+    void *v;
+    float *k_scale;
+    float *v_scale;
+    int64_t layer_stride;
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t token_stride;
+    int32_t dtype;
+    int32_t layers;
+    int32_t pages;
+    int32_t kv_heads;
+    int32_t page_size;
+    int32_t head_dim;
+} bitnet_kv_cache;
+
+/* The pages of `rows` requests.  tables[r][i] is the page of tokens
+ * [i*page_size, (i+1)*page_size) of request r; owned[r][] lists the pages that
+ * were allocated to request r, which differ from its table's once beams share
+ * pages; free_pages is a stack of unused pages (capacity `pages`).  All are
+ * int32 device arrays; rows 1..4096, max_pages * page_size < 2^31. */
+typedef struct bitnet_kv_pool {
+    int32_t *tables;       /* [rows][max_pages] */
+    int32_t *owned;        /* [rows][max_pages] */
+    int32_t *free_pages;   /* [pages]           */
+    int32_t rows;
+    int32_t max_pages;
+    int32_t pages;
+    int32_t page_size;
+} bitnet_kv_pool;
+
+#define BITNET_MAX_ROWS 4096
+
+/* bitnet_kv_map: one step's tokens.  new_lens[r] > 0 adds that many tokens to
+ *   request r, 0 leaves it, a negative value ends it.
+ *   state    int32 [2*rows + 1]: the requests' lengths in tokens, their counts
+ *            of owned pages, and the number of free pages.  Read from state_in
+ *            and written to state_out (which may be the same array).
+ *   First the pages owned by ended requests are pushed on the stack, in
+ *   request order and, per request, in the order of allocation; their length
+ *   and count become 0.  Then request r with length L gets
+ *   ceil((L + n) / page_size) - ceil(L / page_size) new pages, from the top of
+ *   the stack in request order, written to its table and appended to owned.
+ *   status[r]: 0 granted; 1 its table or owned list would overflow; 2 out of
+ *   pages: the needs of the requests up to r, those with status 1 left out,
+ *   exceed the stack; 3 the same for tokens and T.  (2 never meets a request
+ *   that needs no page, 3 none that adds no token.)  A request that is not
+ *   granted keeps its length and adds nothing.
+ *   Outputs: starts int32 [rows + 1], the tokens granted before each request;
+ *   for the tokens in request order slots, positions and rows int32 [T]: slot
+ *   in the cache, position in the request, request.  Entries behind the last
+ *   token are -1.  slots is -1 too where the table's page is out of range.
+ *   Lengths, counts and the stack's height are clamped to their ranges first.
+ *   1 <= T < 2^31.  One launch, or two for T > 8192.  No output may overlap
+ *   another array.
+ */
+bitnet_status bitnet_kv_map(const bitnet_kv_pool *pool, int64_t T, const int32_t *new_lens,
+                            const int32_t *state_in, int32_t *state_out, int32_t *starts,
+                            int32_t *slots, int32_t *positions, int32_t *rows, int32_t *status,
+                            void *stream);
+
+/* bitnet_kv_append: the new tokens of one layer.  Row t of k and v (fp32
+ *   [T][kv_heads*head_dim], rows k_stride and v_stride elements apart) goes to
+ *   slot slots[t].  With cos and sin (fp32 [max_pos][head_dim/2]) k and the
+ *   query heads q (fp32, q_heads*head_dim per row, rows q_stride apart) are
+ *   rotated by the position p = positions[t] first: channels i and
+ *   i + head_dim/2 of a head, a and b, become
+ *   fl32(a*cos[p][i] - b*sin[p][i]) and fl32(b*cos[p][i] + a*sin[p][i]), the
+ *   sums taken in fp64 (each rounded once to fp64, once to fp32); q_out fp32
+ *   [T][q_heads*head_dim] takes the rotated queries.  q (then q_out too) may
+ *   be NULL to rotate only k; without cos and sin (both NULL) nothing is
+ *   rotated, positions may be NULL and q and q_out have to be.
+ *   The stored value is the rounded (half to even) or quantized fp32 row.
+ *   A token whose slot is outside [0, pages*page_size), or whose position is
+ *   outside [0, max_pos) where it is used, is skipped: nothing of it is
+ *   written, q_out included.  Slots of one call must differ from each other.
+ *   T == 0 launches nothing.  q_out == q is allowed for contiguous rows; other
+ *   overlaps are BITNET_ERR_ALIAS.  q, k, v, q_out, cos and sin 16-byte
+ *   aligned, row strides multiples of 4 and below 2^31 elements; T,
+ *   q_heads*head_dim and max_pos below 2^23.  One launch.
+ */
+bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, int32_t layer, int64_t T,
+                               int64_t q_heads, const float *k, int64_t k_stride, const float *v,
+                               int64_t v_stride, const int32_t *slots, const int32_t *positions,
+                               const float *cos, const float *sin, int64_t max_pos,
+                               const float *q, int64_t q_stride, float *q_out, void *stream);
+
+/* bitnet_paged_attention: row t attends to the first lens[t] tokens of table
+ *   row r = rows[t] (rows NULL: r = t, T <= table_rows):
+ *     out[t][h] = sum_j p_j v_j,  p = softmax_j(scale * q[t][h] . k_j),
+ *   query head h with key/value head h / (q_heads / kv_heads); q fp32
+ *   (q_heads*head_dim per row, rows q_stride apart), out fp32
+ *   [T][q_heads*head_dim]; lse (optional) fp32 [T][q_heads] the natural
+ *   logarithm of the softmax's denominator.  Sums, maxima and outputs are held
+ *   in fp32; queries and probabilities meet the cache's values on the matrix
+ *   cores as sums of two or three 16-bit terms that together carry fp32's
+ *   precision.
+ *   tables int32 [table_rows][max_pages].  lens is clamped to [0, max_len];
+ *   max_len <= max_pages * page_size is the host's bound, which sizes the
+ *   split of the length.  A token whose page is outside [0, pages) is left
+ *   out.  Table entries behind the length, slots behind it and their scales
+ *   are never used, whatever they hold.  A row without tokens (length 0, or
+ *   rows[t] outside [0, table_rows)) gives zeros and lse -inf.
+ *   q_heads a multiple of kv_heads, at most 64 per kv head; T and table_rows
+ *   below 2^23, max_len and max_pages below 2^31; q and out 16-byte aligned,
+ *   q_stride a multiple of 4 and below 2^31.
+ *   T == 0 launches nothing.  out, lse and the inputs must not overlap.
+ *   workspace: bitnet_paged_attention_workspace_bytes(...) bytes, 256-byte
+ *   aligned, ZERO-FILLED before its first use and written by nothing else
+ *   (its first 16 KB hold counters that every call leaves at zero; calls of
+ *   any shapes may follow each other on one workspace, none may overlap in
+ *   time).  One launch.
+ */
+size_t bitnet_paged_attention_workspace_bytes(int64_t T, int64_t q_heads, int64_t kv_heads,
+                                              int64_t head_dim, int64_t max_len);
+
+bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer, int64_t T,
+                                     int64_t q_heads, const float *q, int64_t q_stride,
+                                     const int32_t *tables, int64_t table_rows,
+                                     int64_t max_pages, const int32_t *rows, const int32_t *lens,
+                                     int64_t max_len, float scale, float *out, float *lse,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* bitnet_beam_select: the next W beams of each of B groups from the logits of
+ *   its W beams, rows of fp32 [B*W][V], ld elements apart.  Candidate (beam w,
+ *   token v) has the score scores_in[w] + logit - lse, lse the natural
+ *   logarithm of the sum of exp over the beam's logits; the W best of the
+ *   group's W*V are taken in descending order.  Scores are compared in fp64
+ *   (the sum of exp has fp32 terms, about 1e-7 relative); where they are equal
+ *   the lower beam goes first, and within a beam the larger logit, then the
+ *   lower token.  W = 1 is greedy decoding.
+ *   Logits of -inf are tokens that cannot be taken; NaN and +inf count as
+ *   -inf, in logits and in scores.  Candidates of score -inf are taken only
+ *   where nothing else is left.
+ *   finished_in (optional, int32 [B*W]): a beam with a nonzero flag has the one
+ *   candidate eos, at its unchanged score, and its logits are not used;
+ *   all its other tokens score -inf (lowest token first).
+ *   Outputs [B*W]: scores_out fp32 (rounded once from fp64), tokens int32,
+ *   parents int32 (row numbers g*W + w), finished_out int32 (given exactly
+ *   when finished_in is): the parent's flag, or token == eos.  scores_out and
+ *   finished_out may be scores_in and finished_in themselves.
+ *   B*W <= 4096, 1 <= W <= 32, W <= V < 2^30, V <= ld < 2^31, 0 <= eos < V when
+ *   finished_in is given.
+ *   workspace: bitnet_beam_select_workspace_bytes(B, W, V) bytes, 256-byte
+ *   aligned, zero-filled before its first use, on the same terms as the
+ *   attention's.  One launch.
+ */
+size_t bitnet_beam_select_workspace_bytes(int64_t B, int64_t W, int64_t V);
+
+bitnet_status bitnet_beam_select(int64_t B, int64_t W, int64_t V, const float *logits, int64_t ld,
+                                 const float *scores_in, const int32_t *finished_in, int32_t eos,
+                                 float *scores_out, int32_t *tokens, int32_t *parents,
+                                 int32_t *finished_out, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* bitnet_beam_reorder: row g*W + j of the new tables continues row
+ *   parents[g*W + j] of its group.  The beams of a group advance together: the
+ *   length of all of them is lens[g*W].  Full pages are shared: their table
+ *   entries are the parent's.  Of a partly filled last page each beam needs
+ *   its own: the parent's first child (in row order) keeps it; every other
+ *   child takes, in row order, the last page of the next beam of the group
+ *   that has no child, and the tokens in use are copied into it, in every
+ *   layer.  (There are as many of the one as of the other.)  So the last pages
+ *   of a group's rows, as passed in, must differ from each other.
+ *   tables_in, tables_out int32 [B*W][max_pages], apart from each other;
+ *   entries behind the length are the row's own from tables_in.  A parent
+ *   outside the group counts as the row itself; lengths are clamped to
+ *   [0, max_pages * page_size]; a copy from or to a page outside [0, pages)
+ *   is left out.  B*W <= 4096, 1 <= W <= 32.  One launch.
+ */
+bitnet_status bitnet_beam_reorder(const bitnet_kv_cache *cache, int64_t B, int64_t W,
+                                  const int32_t *parents, const int32_t *lens,
+                                  const int32_t *tables_in, int32_t *tables_out,
+                                  int64_t max_pages, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

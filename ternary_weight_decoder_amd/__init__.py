@@ -12,6 +12,9 @@ _BINDING_NAMES = {
     "bitnet_ternary_matmul_q8", "bitnet_ternary_matmul_grouped", "GroupedPlan",
     "BitnetError", "bitnet_packed_bytes", "bitnet_matmul_workspace_bytes",
     "bitnet_ternarize_workspace_bytes", "bitnet_grouped_workspace_bytes",
+    "KvCache", "KvPool", "bitnet_kv_map", "bitnet_kv_append", "bitnet_paged_attention",
+    "bitnet_beam_select", "bitnet_beam_reorder",
+    "bitnet_paged_attention_workspace_bytes", "bitnet_beam_select_workspace_bytes",
 }
 
 

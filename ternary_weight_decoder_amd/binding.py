@@ -7,6 +7,7 @@ is not a gfx950, calls raise -- there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -36,6 +37,18 @@ class BitnetError(RuntimeError):
 class bitnet_problem(ctypes.Structure):
     _fields_ = [("x", _p), ("packed", _p), ("w_scale", _p), ("y", _p),
                 ("N", _i64), ("K", _i64)]
+
+
+class bitnet_kv_cache(ctypes.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p),
+                ("layer_stride", _i64), ("page_stride", _i64), ("head_stride", _i64),
+                ("token_stride", _i64), ("dtype", _i32), ("layers", _i32), ("pages", _i32),
+                ("kv_heads", _i32), ("page_size", _i32), ("head_dim", _i32)]
+
+
+class bitnet_kv_pool(ctypes.Structure):
+    _fields_ = [("tables", _p), ("owned", _p), ("free_pages", _p), ("rows", _i32),
+                ("max_pages", _i32), ("pages", _i32), ("page_size", _i32)]
 
 
 EXPORTS = (
@@ -125,6 +138,23 @@ def lib():
         L.bitnet_embed_lookup.restype = _i32
         L.bitnet_lm_head.argtypes = [_i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p, _p]
         L.bitnet_lm_head.restype = _i32
+        L.bitnet_kv_map.argtypes = [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _p]
+        L.bitnet_kv_map.restype = _i32
+        L.bitnet_kv_append.argtypes = [_p, _i32, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p,
+                                       _i64, _p, _i64, _p, _p]
+        L.bitnet_kv_append.restype = _i32
+        L.bitnet_paged_attention_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _i64]
+        L.bitnet_paged_attention_workspace_bytes.restype = _sz
+        L.bitnet_paged_attention.argtypes = [_p, _i32, _i64, _i64, _p, _i64, _p, _i64, _i64, _p,
+                                             _p, _i64, _c.c_float, _p, _p, _p, _sz, _p]
+        L.bitnet_paged_attention.restype = _i32
+        L.bitnet_beam_select_workspace_bytes.argtypes = [_i64, _i64, _i64]
+        L.bitnet_beam_select_workspace_bytes.restype = _sz
+        L.bitnet_beam_select.argtypes = [_i64, _i64, _i64, _p, _i64, _p, _p, _i32, _p, _p, _p, _p,
+                                         _p, _sz, _p]
+        L.bitnet_beam_select.restype = _i32
+        L.bitnet_beam_reorder.argtypes = [_p, _i64, _i64, _p, _p, _p, _p, _i64, _p]
+        L.bitnet_beam_reorder.restype = _i32
         _lib = L
     return _lib
 
@@ -617,3 +647,303 @@ class StagedPlan:
     def timeouts_total(self) -> int:
         """Calls with a wait that ran out, since the workspace was zero-filled."""
         return int(self.workspace[8:12].view(torch.int32).item())
+
+
+# ---- the paged key-value cache and beam search ------------------------------
+
+KV_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.int8: 2}
+
+
+class KvCache:
+    """The keys and values of all layers in pages.
+
+    k, v: device tensors [layers, pages, kv_heads, page_size, head_dim] of
+    bfloat16, float16 or int8, with equal strides and contiguous channels (heads
+    before tokens in memory, or a transposed view of tokens before heads).
+    int8 caches carry fp32 scales k_scale, v_scale [layers, pages, kv_heads,
+    page_size].  Holds the descriptor that the calls pass to the library.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale=None, v_scale=None):
+        if k.dtype not in KV_DTYPES:
+            raise ValueError(f"cache dtype must be one of {list(KV_DTYPES)}, got {k.dtype}")
+        if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be [layers, pages, kv_heads, page_size, head_dim] alike")
+        layers, pages, heads, page, dim = k.shape
+        if not (k.is_cuda and v.device == k.device):
+            raise ValueError("k and v must be device tensors of one device")
+        # strides of axes of one entry are never used and may be anything
+        if any(n > 1 and a != b for n, a, b in zip(k.shape, k.stride(), v.stride())):
+            raise ValueError("k and v must have equal strides")
+        if dim > 1 and k.stride(4) != 1:
+            raise ValueError("channels must be contiguous")
+        if (k.dtype is torch.int8) != (k_scale is not None and v_scale is not None) or (
+                (k_scale is None) != (v_scale is None)):
+            raise ValueError("int8 caches, and no others, take k_scale and v_scale")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None:
+                _dev(t, torch.float32, name)
+                if t.shape != k.shape[:4] or t.device != k.device:
+                    raise ValueError(f"{name} must be [layers, pages, kv_heads, page_size]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.layers, self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        st = [s if n > 1 else max(dim, 16) for n, s in zip(k.shape, k.stride())]
+        self.c = bitnet_kv_cache(
+            k.data_ptr(), v.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
+            0 if v_scale is None else v_scale.data_ptr(), st[0], st[1], st[2], st[3],
+            KV_DTYPES[k.dtype], layers, pages, heads, page, dim)
+        self.ref = _c.byref(self.c)
+
+    @classmethod
+    def empty(cls, layers: int, pages: int, kv_heads: int, page_size: int, head_dim: int,
+              dtype=torch.bfloat16, device="cuda"):
+        """A cache of uninitialized pages, heads before tokens."""
+        shape = (layers, pages, kv_heads, page_size, head_dim)
+        k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        if dtype is not torch.int8:
+            return cls(k, v)
+        return cls(k, v, *(torch.empty(shape[:4], dtype=torch.float32, device=device)
+                           for _ in range(2)))
+
+
+class KvPool:
+    """The pages of a set of requests: block tables, the pages each request
+    owns and the stack of unused pages (int32 device tensors)."""
+
+    def __init__(self, pages: int, page_size: int, tables: torch.Tensor, owned: torch.Tensor,
+                 free_pages: torch.Tensor):
+        for t, name in ((tables, "tables"), (owned, "owned"), (free_pages, "free_pages")):
+            _dev(t, torch.int32, name)
+        if tables.dim() != 2 or owned.shape != tables.shape or free_pages.numel() != pages:
+            raise ValueError("tables and owned are [rows, max_pages], free_pages [pages]")
+        self.tables, self.owned, self.free_pages = tables, owned, free_pages
+        self.rows, self.max_pages = tables.shape
+        self.pages, self.page_size = int(pages), int(page_size)
+        self.c = bitnet_kv_pool(tables.data_ptr(), owned.data_ptr(), free_pages.data_ptr(),
+                                self.rows, self.max_pages, self.pages, self.page_size)
+        self.ref = _c.byref(self.c)
+
+    @classmethod
+    def empty(cls, rows: int, max_pages: int, pages: int, page_size: int, device="cuda"):
+        """(pool, state) of requests without tokens; all pages are free, and
+        the lowest numbered ones are handed out first."""
+        i32 = dict(dtype=torch.int32, device=device)
+        tables, owned = (torch.full((rows, max_pages), -1, **i32) for _ in range(2))
+        free = torch.arange(pages - 1, -1, -1, **i32)
+        state = torch.zeros(2 * rows + 1, **i32)
+        state[-1] = pages
+        return cls(pages, page_size, tables, owned, free), state
+
+
+def bitnet_kv_map_into(pool: KvPool, T, new_lens, state_in, state_out, starts, slots, positions,
+                       rows, status, stream=None) -> None:
+    _check(lib().bitnet_kv_map(pool.ref, T, _ptr(new_lens), _ptr(state_in), _ptr(state_out),
+                               _ptr(starts), _ptr(slots), _ptr(positions), _ptr(rows),
+                               _ptr(status), _stream(stream)),
+           "bitnet_kv_map")
+
+
+def _rows_stride(t, width):
+    """Elements between the rows of a [T, width] tensor with contiguous rows."""
+    return t.stride(0) if t.shape[0] > 1 else max(width, 4)
+
+
+def bitnet_kv_append_into(cache: KvCache, layer, T, q_heads, k, v, slots, positions=None, cos=None,
+                          sin=None, q=None, q_out=None, stream=None) -> None:
+    w = cache.kv_heads * cache.head_dim
+    _check(lib().bitnet_kv_append(cache.ref, layer, T, q_heads, _ptr(k), _rows_stride(k, w),
+                                  _ptr(v), _rows_stride(v, w), _ptr(slots), _ptr(positions),
+                                  _ptr(cos), _ptr(sin), 0 if cos is None else cos.shape[0],
+                                  _ptr(q),
+                                  0 if q is None else _rows_stride(q, q_heads * cache.head_dim),
+                                  _ptr(q_out), _stream(stream)),
+           "bitnet_kv_append")
+
+
+def bitnet_paged_attention_workspace_bytes(T: int, q_heads: int, kv_heads: int, head_dim: int,
+                                           max_len: int) -> int:
+    return int(lib().bitnet_paged_attention_workspace_bytes(T, q_heads, kv_heads, head_dim,
+                                                            max_len))
+
+
+def bitnet_paged_attention_into(cache: KvCache, layer, T, q_heads, q, tables, lens, max_len, scale,
+                                out, workspace, rows=None, lse=None, stream=None) -> None:
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().bitnet_paged_attention(cache.ref, layer, T, q_heads, _ptr(q),
+                                        _rows_stride(q, q_heads * cache.head_dim), _ptr(tables),
+                                        tables.shape[0], tables.shape[1], _ptr(rows), _ptr(lens),
+                                        max_len, scale, _ptr(out), _ptr(lse), _ptr(workspace),
+                                        ws_bytes, _stream(stream)),
+           "bitnet_paged_attention")
+
+
+def bitnet_beam_select_workspace_bytes(B: int, W: int, V: int) -> int:
+    return int(lib().bitnet_beam_select_workspace_bytes(B, W, V))
+
+
+def bitnet_beam_select_into(B, W, V, logits, scores_in, finished_in, eos, scores_out, tokens,
+                            parents, finished_out, workspace, stream=None) -> None:
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().bitnet_beam_select(B, W, V, _ptr(logits), _rows_stride(logits, V),
+                                    _ptr(scores_in), _ptr(finished_in), eos, _ptr(scores_out),
+                                    _ptr(tokens), _ptr(parents), _ptr(finished_out),
+                                    _ptr(workspace), ws_bytes, _stream(stream)),
+           "bitnet_beam_select")
+
+
+def bitnet_beam_reorder_into(cache: KvCache, B, W, parents, lens, tables_in, tables_out,
+                             stream=None) -> None:
+    _check(lib().bitnet_beam_reorder(cache.ref, B, W, _ptr(parents), _ptr(lens), _ptr(tables_in),
+                                     _ptr(tables_out), tables_in.shape[1], _stream(stream)),
+           "bitnet_beam_reorder")
+
+
+# Convenience forms: arguments checked against the cache's and the pool's
+# shapes, outputs (and workspaces) allocated with torch on the stream that runs
+# the call.
+
+def _on(stream):
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _here(dev: torch.device) -> None:
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors of {dev}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _arg(t: torch.Tensor, dtype, shape, dev: torch.device, name: str) -> None:
+    _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _rows_arg(t: torch.Tensor, T: int, width: int, dev: torch.device, name: str) -> None:
+    """fp32 [T, width] whose rows are contiguous and may lie apart."""
+    if not t.is_cuda or t.dtype != torch.float32 or t.device != dev:
+        raise ValueError(f"{name} must be a torch.float32 tensor on {dev}")
+    if t.dim() != 2 or tuple(t.shape) != (T, width) or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{T}, {width}] with contiguous rows")
+
+
+def bitnet_kv_map(pool: KvPool, T: int, new_lens: torch.Tensor, state: torch.Tensor, stream=None):
+    """One step's tokens: new_lens int32 [rows] (tokens to add, 0, or negative to
+    end a request) and state int32 [2*rows + 1], which is updated in place ->
+    dict of starts [rows + 1], slots, positions, rows [T] and status [rows]."""
+    dev = pool.tables.device
+    _here(dev)
+    _arg(new_lens, torch.int32, (pool.rows,), dev, "new_lens")
+    _arg(state, torch.int32, (2 * pool.rows + 1,), dev, "state")
+    with _on(stream):
+        out = {n: torch.empty(c, dtype=torch.int32, device=dev)
+               for n, c in (("starts", pool.rows + 1), ("slots", T), ("positions", T), ("rows", T),
+                            ("status", pool.rows))}
+        bitnet_kv_map_into(pool, T, new_lens, state, state, *out.values(), stream=stream)
+    return out
+
+
+def bitnet_kv_append(cache: KvCache, layer: int, k: torch.Tensor, v: torch.Tensor,
+                     slots: torch.Tensor, positions=None, cos=None, sin=None, q=None, stream=None):
+    """Write fp32 rows k, v [T, kv_heads*head_dim] to the slots of one layer; with
+    cos and sin [max_pos, head_dim/2] k and q [T, q_heads*head_dim] are rotated
+    by their positions first.  Returns the rotated q (None without q)."""
+    dev, D = cache.k.device, cache.head_dim
+    _here(dev)
+    T = k.shape[0]
+    _rows_arg(k, T, cache.kv_heads * D, dev, "k")
+    _rows_arg(v, T, cache.kv_heads * D, dev, "v")
+    _arg(slots, torch.int32, (T,), dev, "slots")
+    if (cos is None) != (sin is None) or (cos is not None and positions is None):
+        raise ValueError("a rotation takes cos, sin and positions")
+    if cos is not None:
+        _arg(cos, torch.float32, (cos.shape[0], D // 2), dev, "cos")
+        _arg(sin, torch.float32, cos.shape, dev, "sin")
+        _arg(positions, torch.int32, (T,), dev, "positions")
+    q_heads, q_out = 0, None
+    with _on(stream):
+        if q is not None:
+            q_heads = q.shape[1] // D
+            _rows_arg(q, T, q_heads * D, dev, "q")
+            q_out = torch.zeros((T, q_heads * D), dtype=torch.float32, device=dev)
+        bitnet_kv_append_into(cache, layer, T, q_heads, k, v, slots, positions, cos, sin, q, q_out,
+                              stream)
+    return q_out
+
+
+def bitnet_paged_attention(cache: KvCache, layer: int, q: torch.Tensor, tables: torch.Tensor,
+                           lens: torch.Tensor, max_len=None, scale=None, rows=None,
+                           return_lse: bool = False, stream=None):
+    """Attention of q fp32 [T, q_heads*head_dim], one new token per row, over the
+    first lens[t] tokens of table row rows[t] (default t).  max_len defaults to
+    what a table holds, scale to head_dim**-0.5.  Returns fp32 [T,
+    q_heads*head_dim] (and the log-sum-exp [T, q_heads])."""
+    dev, D = cache.k.device, cache.head_dim
+    _here(dev)
+    T, width = q.shape
+    _rows_arg(q, T, width, dev, "q")
+    if width % (cache.kv_heads * D):
+        raise ValueError("q's width must be a multiple of kv_heads*head_dim")
+    if tables.dim() != 2:
+        raise ValueError("tables must be [rows, max_pages]")
+    _arg(tables, torch.int32, tables.shape, dev, "tables")
+    _arg(lens, torch.int32, (T,), dev, "lens")
+    if rows is not None:
+        _arg(rows, torch.int32, (T,), dev, "rows")
+    if max_len is None:
+        max_len = tables.shape[1] * cache.page_size
+    H = width // D
+    with _on(stream):
+        out = torch.empty((T, width), dtype=torch.float32, device=dev)
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev) if return_lse else None
+        ws = torch.zeros(bitnet_paged_attention_workspace_bytes(T, H, cache.kv_heads, D, max_len),
+                         dtype=torch.uint8, device=dev)
+        bitnet_paged_attention_into(cache, layer, T, H, q, tables, lens, max_len,
+                                    D ** -0.5 if scale is None else scale, out, ws, rows, lse,
+                                    stream)
+    return (out, lse) if return_lse else out
+
+
+def bitnet_beam_select(logits: torch.Tensor, scores: torch.Tensor, W: int, finished=None,
+                       eos: int = -1, stream=None):
+    """The next W beams of each group: fp32 logits [B*W, V] (rows may lie apart),
+    scores [B*W], optional finished flags int32 [B*W] with the end token eos ->
+    dict of scores, tokens, parents (row numbers) and, with finished, finished."""
+    dev = logits.device
+    _here(dev)
+    R, V = logits.shape
+    _rows_arg(logits, R, V, dev, "logits")
+    if W < 1 or R % W:
+        raise ValueError("logits rows must be a multiple of W")
+    _arg(scores, torch.float32, (R,), dev, "scores")
+    if finished is not None:
+        _arg(finished, torch.int32, (R,), dev, "finished")
+    with _on(stream):
+        out = {"scores": torch.empty(R, dtype=torch.float32, device=dev)}
+        for n in ("tokens", "parents") + (("finished",) if finished is not None else ()):
+            out[n] = torch.empty(R, dtype=torch.int32, device=dev)
+        ws = torch.zeros(bitnet_beam_select_workspace_bytes(R // W, W, V), dtype=torch.uint8,
+                         device=dev)
+        bitnet_beam_select_into(R // W, W, V, logits, scores, finished, eos, out["scores"],
+                                out["tokens"], out["parents"], out.get("finished"), ws, stream)
+    return out
+
+
+def bitnet_beam_reorder(cache: KvCache, tables: torch.Tensor, lens: torch.Tensor,
+                        parents: torch.Tensor, W: int, stream=None):
+    """The block tables [B*W, max_pages] of the beams that continue parents
+    (row numbers); partly filled last pages are copied inside the cache.
+    Returns new tables; the old ones are unchanged."""
+    dev = cache.k.device
+    _here(dev)
+    if tables.dim() != 2 or W < 1 or tables.shape[0] % W:
+        raise ValueError("tables must be [B*W, max_pages]")
+    R = tables.shape[0]
+    _arg(tables, torch.int32, tables.shape, dev, "tables")
+    _arg(lens, torch.int32, (R,), dev, "lens")
+    _arg(parents, torch.int32, (R,), dev, "parents")
+    with _on(stream):
+        out = torch.empty_like(tables)
+        bitnet_beam_reorder_into(cache, R // W, W, parents, lens, tables, out, stream)
+    return out

@@ -11,6 +11,7 @@
 
 #include "bitnet_internal.hpp"
 #include "bitnet_variants.hpp"
+#include "kv.hpp"
 #include "bitnet_tm.h"
 
 using namespace bitnet;
@@ -793,6 +794,335 @@ bitnet_status bitnet_ternary_matmul_stages(int64_t M, const bitnet_problem *prob
 
   return from_hip(launch_stages(problems_dev, problems_host, count, stage_end, nstages, (int)M,
                                 src, reinterpret_cast<uint8_t *>(workspace), as_stream(stream)));
+}
+
+// ---- the paged key-value cache and beam search -----------------------------
+
+// An array of a call, for the overlap checks.
+struct Range {
+  const void *p;
+  int64_t bytes;
+};
+
+static bool overlap(const Range &a, const Range &b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return a.p && b.p && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+
+// The first `nout` ranges are written: none may overlap any other range.
+static bool overlaps_any(const Range *r, int nout, int n) {
+  for (int i = 0; i < nout; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (overlap(r[i], r[j])) return true;
+  return false;
+}
+
+static bool power_of_two(int64_t v) { return v >= 1 && (v & (v - 1)) == 0; }
+
+static int shift_of(int64_t v) {
+  int s = 0;
+  while (((int64_t)1 << s) < v) ++s;
+  return s;
+}
+
+constexpr int64_t kMaxStride = (int64_t)1 << 40;   // of the cache, elements
+constexpr int64_t kMaxTokens = kLimit / 256;       // rows of one call
+constexpr int64_t kMaxVocab = kLimit / 2;
+
+static bitnet_status check_cache(const bitnet_kv_cache *c, int32_t layer) {
+  if (!c || !c->k || !c->v) return BITNET_ERR_NULL;
+  const bool i8 = c->dtype == BITNET_KV_INT8;
+  if (!i8 && c->dtype != BITNET_KV_BF16 && c->dtype != BITNET_KV_FP16) return BITNET_ERR_SHAPE;
+  if (i8 && (!c->k_scale || !c->v_scale)) return BITNET_ERR_NULL;
+  const int D = c->head_dim;
+  if (D != 64 && D != 128 && D != 256) return BITNET_ERR_SHAPE;
+  if (!power_of_two(c->page_size) || c->page_size > 1024) return BITNET_ERR_SHAPE;
+  if (c->layers < 1 || c->layers > 1024 || layer < 0 || layer >= c->layers)
+    return BITNET_ERR_SHAPE;
+  if (c->kv_heads < 1 || c->kv_heads > 256 || c->pages < 1 ||
+      (int64_t)c->pages * c->page_size >= kLimit)
+    return BITNET_ERR_SHAPE;
+  const int64_t per16 = i8 ? 16 : 8;   // elements in 16 bytes
+  const int64_t strides[4] = {c->page_stride, c->head_stride, c->token_stride,
+                              c->layers > 1 ? c->layer_stride : c->page_stride};
+  for (const int64_t s : strides) {
+    if (s < D || s >= kMaxStride) return BITNET_ERR_SHAPE;
+    if (s % per16 != 0) return BITNET_ERR_ALIGN;
+  }
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return BITNET_ERR_ALIGN;
+  if (i8 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))) return BITNET_ERR_ALIGN;
+  return BITNET_OK;
+}
+
+static KvView kv_view(const bitnet_kv_cache *c, int32_t layer) {
+  const bool i8 = c->dtype == BITNET_KV_INT8;
+  const int64_t off = layer ? layer * c->layer_stride * (i8 ? 1 : 2) : 0;
+  const int64_t soff = (int64_t)layer * c->pages * c->kv_heads * c->page_size;
+  KvView v;
+  v.k = static_cast<uint8_t *>(c->k) + off;
+  v.v = static_cast<uint8_t *>(c->v) + off;
+  v.k_scale = i8 ? c->k_scale + soff : nullptr;
+  v.v_scale = i8 ? c->v_scale + soff : nullptr;
+  v.page_stride = c->page_stride;
+  v.head_stride = c->head_stride;
+  v.token_stride = c->token_stride;
+  v.pages = c->pages;
+  v.kv_heads = c->kv_heads;
+  v.page_shift = shift_of(c->page_size);
+  return v;
+}
+
+bitnet_status bitnet_kv_map(const bitnet_kv_pool *pool, int64_t T, const int32_t *new_lens,
+                            const int32_t *state_in, int32_t *state_out, int32_t *starts,
+                            int32_t *slots, int32_t *positions, int32_t *rows, int32_t *status,
+                            void *stream) {
+  if (!pool || !pool->tables || !pool->owned || !pool->free_pages || !new_lens || !state_in ||
+      !state_out || !starts || !slots || !positions || !rows || !status)
+    return BITNET_ERR_NULL;
+  const int64_t B = pool->rows, mp = pool->max_pages, ps = pool->page_size;
+  if (B < 1 || B > kMaxRows || mp < 1 || pool->pages < 1 || !power_of_two(ps) || ps > 1024 ||
+      mp * ps >= kLimit || pool->pages * ps >= kLimit || T < 1 || T >= kLimit)
+    return BITNET_ERR_SHAPE;
+  const void *ptrs[] = {pool->tables, pool->owned, pool->free_pages, state_out, starts, slots,
+                        positions, rows, status, new_lens, state_in};
+  for (const void *p : ptrs)
+    if (!aligned(p, 4)) return BITNET_ERR_ALIGN;
+  const Range r[] = {{pool->tables, B * mp * 4}, {pool->owned, B * mp * 4},
+                     {pool->free_pages, (int64_t)pool->pages * 4}, {state_out, (2 * B + 1) * 4},
+                     {starts, (B + 1) * 4}, {slots, T * 4}, {positions, T * 4}, {rows, T * 4},
+                     {status, B * 4}, {new_lens, B * 4},
+                     {state_in == state_out ? nullptr : state_in, (2 * B + 1) * 4}};
+  if (overlaps_any(r, 9, 11)) return BITNET_ERR_ALIAS;
+  bitnet_status st = device_check();
+  if (st != BITNET_OK) return st;
+  KvMapArgs a;
+  a.new_lens = new_lens;
+  a.state_in = state_in;
+  a.state_out = state_out;
+  a.starts = starts;
+  a.slots = slots;
+  a.positions = positions;
+  a.rows = rows;
+  a.status = status;
+  a.tables = pool->tables;
+  a.owned = pool->owned;
+  a.free_pages = pool->free_pages;
+  a.B = (int32_t)B;
+  a.max_pages = pool->max_pages;
+  a.pages = pool->pages;
+  a.page_shift = shift_of(ps);
+  a.T = T;
+  return from_hip(launch_kv_map(a, as_stream(stream)));
+}
+
+bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, int32_t layer, int64_t T,
+                               int64_t q_heads, const float *k, int64_t k_stride, const float *v,
+                               int64_t v_stride, const int32_t *slots, const int32_t *positions,
+                               const float *cos, const float *sin, int64_t max_pos,
+                               const float *q, int64_t q_stride, float *q_out, void *stream) {
+  bitnet_status st = check_cache(cache, layer);
+  if (st != BITNET_OK) return st;
+  if (T == 0) return BITNET_OK;
+  if (!k || !v || !slots) return BITNET_ERR_NULL;
+  const bool rotate = cos != nullptr;
+  if (rotate != (sin != nullptr) || (rotate && !positions) || (q != nullptr) != (q_out != nullptr))
+    return BITNET_ERR_NULL;
+  if (q && !rotate) return BITNET_ERR_NULL;
+  const int64_t D = cache->head_dim, kd = cache->kv_heads * D, qd = q ? q_heads * D : 0;
+  if (T < 0 || T >= kMaxTokens || (q && (q_heads < 1 || q_heads >= kMaxTokens / D)) ||
+      (rotate && (max_pos < 1 || max_pos >= kMaxTokens)))
+    return BITNET_ERR_SHAPE;
+  if (k_stride < kd || v_stride < kd || (q && q_stride < qd) || k_stride >= kLimit ||
+      v_stride >= kLimit || (q && q_stride >= kLimit))
+    return BITNET_ERR_SHAPE;
+  if (k_stride % 4 || v_stride % 4 || (q && q_stride % 4) || !aligned(k, 16) || !aligned(v, 16) ||
+      !aligned(slots, 4) ||
+      (rotate && (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(positions, 4))) ||
+      (q && (!aligned(q, 16) || !aligned(q_out, 16))))
+    return BITNET_ERR_ALIGN;
+  if (q) {
+    const bool in_place = q_out == q && q_stride == qd;
+    const Range r[] = {{q_out, T * qd * 4},
+                       {in_place ? nullptr : q, ((T - 1) * q_stride + qd) * 4},
+                       {k, ((T - 1) * k_stride + kd) * 4},
+                       {v, ((T - 1) * v_stride + kd) * 4},
+                       {slots, T * 4},
+                       {positions, T * 4},
+                       {cos, max_pos * D * 2},
+                       {sin, max_pos * D * 2}};
+    if (overlaps_any(r, 1, 8)) return BITNET_ERR_ALIAS;
+  }
+  st = device_check();
+  if (st != BITNET_OK) return st;
+  KvAppendArgs a;
+  a.c = kv_view(cache, layer);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.cos = cos;
+  a.sin = sin;
+  a.q_out = q_out;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.slots = slots;
+  a.positions = positions;
+  a.q_heads = (int32_t)(q ? q_heads : 0);
+  a.max_pos = (int32_t)max_pos;
+  a.T = T;
+  return from_hip(launch_kv_append(a, cache->dtype, cache->head_dim, as_stream(stream)));
+}
+
+// Shapes of an attention call, apart from the cache's own.
+static bool attend_shape_ok(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D,
+                            int64_t max_len) {
+  if (T < 1 || T >= kMaxTokens || kv_heads < 1 || kv_heads > 256 || q_heads < 1 ||
+      q_heads % kv_heads != 0 || q_heads / kv_heads > 64)
+    return false;
+  return (D == 64 || D == 128 || D == 256) && max_len >= 1 && max_len < kLimit;
+}
+
+size_t bitnet_paged_attention_workspace_bytes(int64_t T, int64_t q_heads, int64_t kv_heads,
+                                              int64_t head_dim, int64_t max_len) {
+  if (!attend_shape_ok(T, q_heads, kv_heads, head_dim, max_len)) return 0;
+  return attend_workspace_bytes(T, q_heads, kv_heads, head_dim, max_len);
+}
+
+bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer, int64_t T,
+                                     int64_t q_heads, const float *q, int64_t q_stride,
+                                     const int32_t *tables, int64_t table_rows,
+                                     int64_t max_pages, const int32_t *rows, const int32_t *lens,
+                                     int64_t max_len, float scale, float *out, float *lse,
+                                     void *workspace, size_t workspace_bytes, void *stream) {
+  bitnet_status st = check_cache(cache, layer);
+  if (st != BITNET_OK) return st;
+  if (T == 0) return BITNET_OK;
+  if (!q || !tables || !lens || !out) return BITNET_ERR_NULL;
+  const int64_t D = cache->head_dim, qd = q_heads * D;
+  if (!attend_shape_ok(T, q_heads, cache->kv_heads, D, max_len) || q_stride < qd ||
+      q_stride >= kLimit || table_rows < 1 || table_rows >= kMaxTokens || max_pages < 1 ||
+      max_pages >= kLimit || max_len > max_pages * cache->page_size || (!rows && T > table_rows))
+    return BITNET_ERR_SHAPE;
+  if (q_stride % 4 || !aligned(q, 16) || !aligned(out, 16) || !aligned(tables, 4) ||
+      !aligned(lens, 4) || (rows && !aligned(rows, 4)) || (lse && !aligned(lse, 4)))
+    return BITNET_ERR_ALIGN;
+  const size_t need = attend_workspace_bytes(T, q_heads, cache->kv_heads, D, max_len);
+  if (!workspace || workspace_bytes < need) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return BITNET_ERR_ALIGN;
+  const Range r[] = {{out, T * qd * 4},
+                     {lse, T * q_heads * 4},
+                     {workspace, (int64_t)need},
+                     {q, ((T - 1) * q_stride + qd) * 4},
+                     {tables, table_rows * max_pages * 4},
+                     {rows, T * 4},
+                     {lens, T * 4}};
+  if (overlaps_any(r, 3, 7)) return BITNET_ERR_ALIAS;
+  st = device_check();
+  if (st != BITNET_OK) return st;
+  AttendArgs a;
+  a.c = kv_view(cache, layer);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.tables = tables;
+  a.rows = rows;
+  a.lens = lens;
+  a.T = (int32_t)T;
+  a.q_heads = (int32_t)q_heads;
+  a.table_rows = (int32_t)table_rows;
+  a.max_pages = (int32_t)max_pages;
+  a.max_len = (int32_t)max_len;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.ws = static_cast<uint8_t *>(workspace);
+  return from_hip(launch_attend(a, cache->dtype, cache->head_dim, as_stream(stream)));
+}
+
+static bool beams_ok(int64_t B, int64_t W) {
+  return B >= 1 && W >= 1 && W <= kMaxWidth && B <= kMaxRows && B * W <= kMaxRows;
+}
+
+size_t bitnet_beam_select_workspace_bytes(int64_t B, int64_t W, int64_t V) {
+  if (!beams_ok(B, W) || V < W || V >= kMaxVocab) return 0;
+  return select_workspace_bytes(B, W, V);
+}
+
+bitnet_status bitnet_beam_select(int64_t B, int64_t W, int64_t V, const float *logits, int64_t ld,
+                                 const float *scores_in, const int32_t *finished_in, int32_t eos,
+                                 float *scores_out, int32_t *tokens, int32_t *parents,
+                                 int32_t *finished_out, void *workspace, size_t workspace_bytes,
+                                 void *stream) {
+  if (!logits || !scores_in || !scores_out || !tokens || !parents ||
+      (finished_in != nullptr) != (finished_out != nullptr))
+    return BITNET_ERR_NULL;
+  if (!beams_ok(B, W) || V < W || V >= kMaxVocab || ld < V || ld >= kLimit ||
+      (finished_in && (eos < 0 || eos >= V)))
+    return BITNET_ERR_SHAPE;
+  const void *ptrs[] = {logits, scores_in, scores_out, tokens, parents, finished_in, finished_out};
+  for (const void *p : ptrs)
+    if (!aligned(p, 4)) return BITNET_ERR_ALIGN;
+  const size_t need = select_workspace_bytes(B, W, V);
+  if (!workspace || workspace_bytes < need) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return BITNET_ERR_ALIGN;
+  const int64_t n = B * W * 4;
+  const Range r[] = {{scores_out, n}, {tokens, n}, {parents, n}, {finished_out, n},
+                     {workspace, (int64_t)need},
+                     {logits, ((B * W - 1) * ld + V) * 4},
+                     {scores_in == scores_out ? nullptr : scores_in, n},
+                     {finished_in == finished_out ? nullptr : finished_in, n}};
+  if (overlaps_any(r, 5, 8)) return BITNET_ERR_ALIAS;
+  bitnet_status st = device_check();
+  if (st != BITNET_OK) return st;
+  SelectArgs a;
+  a.logits = logits;
+  a.scores_in = scores_in;
+  a.finished_in = finished_in;
+  a.scores_out = scores_out;
+  a.tokens = tokens;
+  a.parents = parents;
+  a.finished_out = finished_out;
+  a.ld = ld;
+  a.B = (int32_t)B;
+  a.W = (int32_t)W;
+  a.V = (int32_t)V;
+  a.eos = eos;
+  a.ws = static_cast<uint8_t *>(workspace);
+  return from_hip(launch_beam_select(a, as_stream(stream)));
+}
+
+bitnet_status bitnet_beam_reorder(const bitnet_kv_cache *cache, int64_t B, int64_t W,
+                                  const int32_t *parents, const int32_t *lens,
+                                  const int32_t *tables_in, int32_t *tables_out,
+                                  int64_t max_pages, void *stream) {
+  bitnet_status st = check_cache(cache, 0);
+  if (st != BITNET_OK) return st;
+  if (!parents || !lens || !tables_in || !tables_out) return BITNET_ERR_NULL;
+  if (!beams_ok(B, W) || max_pages < 1 || max_pages * cache->page_size >= kLimit ||
+      max_pages >= kLimit)
+    return BITNET_ERR_SHAPE;
+  if (!aligned(parents, 4) || !aligned(lens, 4) || !aligned(tables_in, 4) ||
+      !aligned(tables_out, 4))
+    return BITNET_ERR_ALIGN;
+  const int64_t n = B * W * 4;
+  const Range r[] = {{tables_out, n * max_pages}, {tables_in, n * max_pages}, {parents, n},
+                     {lens, n}};
+  if (overlaps_any(r, 1, 4)) return BITNET_ERR_ALIAS;
+  st = device_check();
+  if (st != BITNET_OK) return st;
+  ReorderArgs a;
+  a.c = kv_view(cache, 0);
+  a.layer_stride = cache->layers > 1 ? cache->layer_stride : 0;
+  a.layers = cache->layers;
+  a.head_dim = cache->head_dim;
+  a.elem_bytes = cache->dtype == BITNET_KV_INT8 ? 1 : 2;
+  a.B = (int32_t)B;
+  a.W = (int32_t)W;
+  a.max_pages = (int32_t)max_pages;
+  a.parents = parents;
+  a.lens = lens;
+  a.tables_in = tables_in;
+  a.tables_out = tables_out;
+  return from_hip(launch_beam_reorder(a, as_stream(stream)));
 }
 
 }  // extern "C"
