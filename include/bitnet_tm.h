@@ -621,7 +621,9 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, int32_t layer, int6
  *   logarithm of the softmax's denominator.  Sums, maxima and outputs are held
  *   in fp32; queries and probabilities meet the cache's values on the matrix
  *   cores as sums of two or three 16-bit terms that together carry fp32's
- *   precision.
+ *   precision (for fp16 and int8 caches down to 2^-38 of a head's largest
+ *   query channel, and of the largest probability, times the largest value
+ *   scale; what lies below counts as zero).
  *   tables int32 [table_rows][max_pages].  lens is clamped to [0, max_len];
  *   max_len <= max_pages * page_size is the host's bound, which sizes the
  *   split of the length.  A token whose page is outside [0, pages) is left
@@ -629,8 +631,9 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, int32_t layer, int6
  *   are never used, whatever they hold.  A row without tokens (length 0, or
  *   rows[t] outside [0, table_rows)) gives zeros and lse -inf.
  *   q_heads a multiple of kv_heads, at most 64 per kv head; T and table_rows
- *   below 2^23, max_len and max_pages below 2^31; q and out 16-byte aligned,
- *   q_stride a multiple of 4 and below 2^31.
+ *   below 2^23, T * kv_heads (times 2, 3, 4 for more than 16, 32, 48 query
+ *   heads per kv head) and max_pages below 2^31, max_len below 2^30; q and out
+ *   16-byte aligned, q_stride a multiple of 4 and below 2^31.
  *   T == 0 launches nothing.  out, lse and the inputs must not overlap.
  *   workspace: bitnet_paged_attention_workspace_bytes(...) bytes, 256-byte
  *   aligned, ZERO-FILLED before its first use and written by nothing else

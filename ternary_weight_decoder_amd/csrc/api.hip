@@ -979,7 +979,8 @@ static bool attend_shape_ok(int64_t T, int64_t q_heads, int64_t kv_heads, int64_
   if (T < 1 || T >= kMaxTokens || kv_heads < 1 || kv_heads > 256 || q_heads < 1 ||
       q_heads % kv_heads != 0 || q_heads / kv_heads > 64)
     return false;
-  return (D == 64 || D == 128 || D == 256) && max_len >= 1 && max_len < kLimit;
+  if (T * kv_heads * ((q_heads / kv_heads + 15) / 16) >= kLimit) return false;
+  return (D == 64 || D == 128 || D == 256) && max_len >= 1 && max_len < kLimit / 2;
 }
 
 size_t bitnet_paged_attention_workspace_bytes(int64_t T, int64_t q_heads, int64_t kv_heads,

@@ -1,9 +1,40 @@
 // Attention of one new token per row over the paged key-value cache.
 //
-// One workgroup per row and query head walks the length in steps of 256
-// tokens: a thread scores one token, the workgroup takes the running maximum
-// and sum of the softmax, and the threads then share the channels of the
-// weighted sum.
+//   s_j = scale * q . k_j,   p_j = exp(s_j - max s),   out = sum p_j v_j / sum p_j
+//
+// The cache is read once and everything else is small, so the kernel is a
+// stream of key and value rows.  A workgroup takes one row t, one key/value
+// head with up to 16 of its query heads, and a part of the row's length; its
+// waves walk 32-token tiles, each with its own running maximum, sum and
+// outputs, and join them in LDS at the end.  Parts of a long row are joined by
+// the workgroup that finishes last.
+//
+// Tile.  Lane L = c + 16h loads, for tokens c and c + 16, the 16-byte pieces
+// h, h + 4, ... of the key row and of the value row: keys and values lie at
+// equal offsets, so a tile costs two addresses per lane.  The keys are, as
+// loaded, the token operand of v_mfma_f32_16x16x32 (row c, eight channels);
+// with the queries as the other operand the scores arrive transposed, lane
+// (c, h) holding head c and tokens 4h..4h+3 (+ 16).  That is the layout in
+// which the second product takes its probabilities, once its 32 contraction
+// steps are numbered to match: steps 8h..8h+3 are tokens 4h.. and steps
+// 8h+4.. tokens 16+4h...  The values need the same order with channels in
+// rows: they go through LDS and come back by the transposing reads, four
+// tokens of one channel per lane.  Nothing else crosses lanes but the tile's
+// maximum (two exchanges).
+//
+// Precision.  The matrix cores multiply 16-bit terms, exactly, into fp32 sums,
+// so queries and probabilities enter as sums of terms: three of bf16 (8 bits
+// each) against bf16 values, two of fp16 (11 bits each) against fp16 values
+// and against 8-bit codes, which are exact in fp16.  fp16's range is made to
+// do by powers of two: queries by their head's largest channel, probabilities
+// by 2^14, and with 8-bit values by the largest value scale so far.
+//
+// While a tile is worked on, the next one's rows are in flight: its keys are
+// asked for once the scores are done with the registers, its values once
+// they are in LDS, its pages a tile earlier.  All loads are unconditional, so
+// that the waits count exactly: a token that is not there (behind the length,
+// or on a page out of range) reads row 0 of page 0 instead; its score becomes
+// -inf and its value zero, whatever memory holds.
 #include <algorithm>
 
 #include "bitnet_device.hpp"
@@ -13,112 +44,494 @@
 namespace bitnet {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-template <int DT> struct KvElem;
-template <> struct KvElem<BITNET_KV_BF16> { typedef __bf16 T; };
-template <> struct KvElem<BITNET_KV_FP16> { typedef _Float16 T; };
-template <> struct KvElem<BITNET_KV_INT8> { typedef int8_t T; };
+#define BITNET_LDS __attribute__((address_space(3)))
 
-__device__ __forceinline__ float block_max(float v, float *red) {
-  v = wave_max(v);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = red[0];
-  for (int w = 1; w < kWaves; ++w) v = fmaxf(v, red[w]);
-  __syncthreads();
-  return v;
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kTile = 32;         // tokens of a wave's step
+constexpr int kHeads = 16;        // query heads of a workgroup
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Tickets of the parts' joins: one counter per (row, head) pair that is split.
+constexpr int kTickets = 4096;
+constexpr int kHeaderBytes = 4 * kTickets;
+
+// How a call is cut: items = rows x key/value heads x groups of 16 query
+// heads, each in up to `parts` parts of at least kMinTiles tiles.
+constexpr int kMinTiles = 16;
+constexpr int kTargetGroups = 2048;
+constexpr int kMaxParts = 64;
+
+struct AttendSplit {
+  int64_t items;
+  int parts;
+  size_t stats, total;   // workspace offsets: partial outputs at kHeaderBytes, then (max, sum)
+};
+
+AttendSplit attend_split(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_len) {
+  const int64_t per = q_heads / kv_heads;
+  AttendSplit s;
+  s.items = T * kv_heads * ((per + kHeads - 1) / kHeads);
+  const int64_t tiles = (max_len + kTile - 1) / kTile;
+  int64_t parts = 1;
+  if (s.items <= kTickets)
+    parts = std::min<int64_t>((kTargetGroups + s.items - 1) / s.items,
+                              (tiles + kMinTiles - 1) / kMinTiles);
+  s.parts = (int)std::max<int64_t>(1, std::min<int64_t>(parts, kMaxParts));
+  const int64_t n = s.parts > 1 ? s.items * s.parts * kHeads : 0;
+  s.stats = kHeaderBytes + (size_t)n * D * 4;
+  s.total = s.stats + (size_t)n * 8;
+  return s;
 }
 
-__device__ __forceinline__ float block_sum(float v, float *red) {
+template <int DT> struct Frag;
+template <> struct Frag<BITNET_KV_BF16> {
+  typedef bf16x8 V;
+  static constexpr int kTerms = 3, kBytes = 2;
+  static constexpr bool kHalf = false;
+  static __device__ __forceinline__ f32x4 mfma(V a, V b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ void split(const float (&x)[8], V (&t)[kTerms]) {
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = red[0];
-  for (int w = 1; w < kWaves; ++w) v += red[w];
-  __syncthreads();
-  return v;
+    for (int e = 0; e < 8; ++e) {
+      float r = x[e];
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i) {
+        t[i][e] = (__bf16)r;
+        r -= (float)t[i][e];
+      }
+    }
+  }
+};
+struct FragF16 {
+  typedef f16x8 V;
+  static constexpr int kTerms = 2;
+  static constexpr bool kHalf = true;
+  static __device__ __forceinline__ f32x4 mfma(V a, V b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ void split(const float (&x)[8], V (&t)[kTerms]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      t[0][e] = (_Float16)x[e];
+      t[1][e] = (_Float16)(x[e] - (float)t[0][e]);
+    }
+  }
+};
+template <> struct Frag<BITNET_KV_FP16> : FragF16 { static constexpr int kBytes = 2; };
+template <> struct Frag<BITNET_KV_INT8> : FragF16 { static constexpr int kBytes = 1; };
+
+// Eight int8 codes as fp16: code + 128 beside the bits of 1024 is 1152 + code,
+// exactly, and the difference to 1152 is exact too.
+__device__ __forceinline__ f16x8 codes_f16(uint32_t lo, uint32_t hi) {
+  f16x8 r;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const uint32_t u = (w ? hi : lo) ^ 0x80808080u;
+    const uint32_t a = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);   // bytes 0, 1
+    const uint32_t b = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);   // bytes 2, 3
+    const f16x2 k = {(_Float16)1152.0f, (_Float16)1152.0f};
+    const f16x2 x = __builtin_bit_cast(f16x2, a) - k, y = __builtin_bit_cast(f16x2, b) - k;
+    r[4 * w] = x.x;
+    r[4 * w + 1] = x.y;
+    r[4 * w + 2] = y.x;
+    r[4 * w + 3] = y.y;
+  }
+  return r;
+}
+
+__device__ __forceinline__ float across4(float v) {   // max over the lanes of one head
+  v = fmaxf(v, __shfl_xor(v, 16, 64));
+  return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float sum4(float v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The power of two above x (x >= 0, below 2^126), at least 2^-100.
+__device__ __forceinline__ float pow2_above(float x) {
+  const uint32_t e = __builtin_bit_cast(uint32_t, x) & 0x7f800000u;
+  const uint32_t lo = (127u - 100u) << 23;
+  return __builtin_bit_cast(float, max(e + 0x00800000u, lo));
+}
+__device__ __forceinline__ float pow2_inverse(float p) {   // of a power of two
+  return __builtin_bit_cast(float, (254u << 23) - __builtin_bit_cast(uint32_t, p));
 }
 
 template <int DT, int D>
-__global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
-  typedef typename KvElem<DT>::T E;
-  __shared__ float q[D], p[kThreads], red[kWaves], part[kThreads];
-  __shared__ int pages[kThreads];
-  const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-  const int kvh = h / (a.q_heads / a.c.kv_heads);
+struct Shape {
+  static constexpr int kBytes = Frag<DT>::kBytes;
+  static constexpr int kPieces = D * kBytes / 64;          // 16-byte pieces per lane and token
+  static constexpr int kRow = D * kBytes + 16;             // value row in LDS
+  static constexpr int kWaveLds = kTile * kRow > kHeads * D * 4 ? kTile * kRow : kHeads * D * 4;
+};
+
+template <int DT, int D>
+struct AttendShared {
+  __attribute__((aligned(16))) uint8_t tile[kWaves][Shape<DT, D>::kWaveLds];
+  float scales[kWaves][2][kTile];      // 8-bit caches: the tile's key and value scales
+  float m[kWaves][kHeads], l[kWaves][kHeads];
+  uint32_t last;
+};
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
+attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
+  typedef Frag<DT> F;
+  typedef typename F::V V;
+  typedef Shape<DT, D> S;
+  constexpr bool kI8 = DT == BITNET_KV_INT8;
+  constexpr int kSteps = D / 32;       // contraction steps of the scores
+  constexpr int kBlocks = D / 16;      // channel blocks of the outputs
+  constexpr float kUp = F::kHalf ? 14.0f : 0.0f;   // probabilities are scaled by 2^kUp
+  __shared__ AttendShared<DT, D> sh;
+
+  const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int per = a.q_heads / a.c.kv_heads;
+  const int groups = (per + kHeads - 1) / kHeads;
+  const int part = blockIdx.x % parts;
+  const int item = blockIdx.x / parts;
+  const int t = item / (a.c.kv_heads * groups);
+  const int kvh = item / groups % a.c.kv_heads;
+  const int head0 = kvh * per + item % groups * kHeads;   // first query head
+  const int nh = min(kHeads, per - item % groups * kHeads);
+
   const int r = a.rows ? a.rows[t] : t;
   const int len = r >= 0 && r < a.table_rows ? min(max(a.lens[t], 0), a.max_len) : 0;
-  const int ps = 1 << a.c.page_shift;
-  if (tid < D) q[tid] = a.q[t * a.q_stride + h * D + tid] * a.scale;
-  __syncthreads();
-  constexpr int kParts = kThreads / D > 0 ? kThreads / D : 1;
-  const int d = tid % D, sub = tid / D;
-  float m = -INFINITY, l = 0.0f, o = 0.0f;
-  for (int j0 = 0; j0 < len; j0 += kThreads) {
-    const int j = j0 + tid;
-    float s = -INFINITY;
-    int page = -1;
-    if (j < len) {
-      page = a.tables[(int64_t)r * a.max_pages + (j >> a.c.page_shift)];
-      if (page < 0 || page >= a.c.pages) page = -1;
+  const int tiles = (len + kTile - 1) / kTile;
+  const int share = max((tiles + parts - 1) / parts, kMinTiles);
+  const int used = max((tiles + share - 1) / share, 1);   // parts with work
+  if (part >= used) return;
+  const int first = part * share, end = min(first + share, tiles);
+
+  // Rows of the cache.
+  const int64_t head_off = (int64_t)kvh * a.c.head_stride * S::kBytes + 16 * h;
+  const uint8_t *kbase = reinterpret_cast<const uint8_t *>(a.c.k) + head_off;
+  const uint8_t *vbase = reinterpret_cast<const uint8_t *>(a.c.v) + head_off;
+  const int32_t *table = a.tables + (int64_t)max(min(r, a.table_rows - 1), 0) * a.max_pages;
+  const int64_t page_bytes = a.c.page_stride * S::kBytes;
+  const int tok_mask = (1 << a.c.page_shift) - 1;
+  const int64_t tok_bytes = a.c.token_stride * S::kBytes;
+
+  int pg[2];                       // pages of tokens c, c + 16 of the tile after the loaded one
+  u32x4 kr[2][S::kPieces], vr[2][S::kPieces];
+  float ksc[2], vsc[2];
+  uint32_t mask, mask_next;        // tokens of the tile that are there
+  int64_t off[2];
+
+  auto load_pages = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = min(tile * kTile + c + 16 * i, len - 1);
+      pg[i] = ld_global<int>(table + (j >> a.c.page_shift));
     }
-    pages[tid] = page;
-    if (page >= 0) {
-      const E *k = reinterpret_cast<const E *>(a.c.k) + page * a.c.page_stride +
-                   kvh * a.c.head_stride + (j & (ps - 1)) * a.c.token_stride;
-      s = 0.0f;
-      for (int i = 0; i < D; ++i) s += q[i] * (float)k[i];
-      if (DT == BITNET_KV_INT8)
-        s *= a.c.k_scale[(((int64_t)page * a.c.kv_heads + kvh) << a.c.page_shift) + (j & (ps - 1))];
+  };
+  auto place = [&](int tile) {   // from pg: row offsets and mask of this tile
+    uint32_t m[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = tile * kTile + c + 16 * i;
+      const bool ok = tile < end && j < len && (uint32_t)pg[i] < (uint32_t)a.c.pages;
+      const int page = ok ? pg[i] : 0, tok = ok ? j & tok_mask : 0;
+      off[i] = page * page_bytes + tok * tok_bytes;
+      if constexpr (kI8) {
+        const int64_t at = (((int64_t)page * a.c.kv_heads + kvh) << a.c.page_shift) + tok;
+        const float ks = ld_global<float>(a.c.k_scale + at), vs = ld_global<float>(a.c.v_scale + at);
+        ksc[i] = ok ? ks : 0.0f;
+        vsc[i] = ok ? vs : 0.0f;
+      }
+      m[i] = (uint32_t)__ballot(ok) & 0xffffu;
     }
-    const float mn = fmaxf(m, block_max(s, red));
-    const float w = mn == -INFINITY ? 0.0f : __expf(s - mn);
-    const float keep = mn == -INFINITY ? 0.0f : __expf(m - mn);
-    l = l * keep + block_sum(w, red);
-    m = mn;
-    p[tid] = w;
-    __syncthreads();
-    o *= keep;
-    const int n = min(kThreads, len - j0);
-    for (int i = sub; i < n; i += kParts) {
-      const int64_t pg = pages[i];
-      if (pg < 0) continue;
-      const int tok = (j0 + i) & (ps - 1);
-      float x = (float)reinterpret_cast<const E *>(a.c.v)[pg * a.c.page_stride +
-                                                          kvh * a.c.head_stride +
-                                                          tok * a.c.token_stride + d];
-      if (DT == BITNET_KV_INT8)
-        x *= a.c.v_scale[((pg * a.c.kv_heads + kvh) << a.c.page_shift) + tok];
-      o += p[i] * x;
+    mask_next = m[0] | (m[1] << 16);
+  };
+  auto load_rows = [&](const uint8_t *base, u32x4 (&x)[2][S::kPieces]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int p = 0; p < S::kPieces; ++p) x[i][p] = ld_global<u32x4>(base + off[i] + 64 * p);
+  };
+
+  float m = -INFINITY, l = 0.0f;
+  f32x4 o[kBlocks];
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) o[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float vmax = pow2_above(0.0f);   // 8-bit caches: o is in units of this
+
+  int tile = first + wave;
+  if (tile < end) {
+    load_pages(tile);
+    place(tile);
+    load_rows(kbase, kr);
+    load_rows(vbase, vr);
+    load_pages(tile + kWaves);
+
+    // Queries as terms.
+    V q[kSteps][F::kTerms];
+    float unscale = 1.0f;
+    {
+      const float *src = a.q + t * a.q_stride + (int64_t)(head0 + min(c, nh - 1)) * D;
+      float x[kSteps][8];
+      float big = 0.0f;
+#pragma unroll
+      for (int f = 0; f < kSteps; ++f) {
+        const int d = kI8 ? (f >> 1) * 64 + 16 * h + (f & 1) * 8 : f * 32 + 8 * h;
+        const f32x4 lo = ld_global<f32x4>(src + d), hi = ld_global<f32x4>(src + d + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[f][e] = lo[e] * (a.scale * kLog2e);
+          x[f][e + 4] = hi[e] * (a.scale * kLog2e);
+          big = fmaxf(big, fmaxf(fabsf(x[f][e]), fabsf(x[f][e + 4])));
+        }
+      }
+      float up = 1.0f;
+      if constexpr (F::kHalf) {
+        const float p2 = pow2_above(across4(big));
+        unscale = p2 * 0x1p-14f;
+        up = pow2_inverse(p2) * 0x1p14f;
+      }
+#pragma unroll
+      for (int f = 0; f < kSteps; ++f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[f][e] *= up;
+        F::split(x[f], q[f]);
+      }
     }
-    __syncthreads();
+
+    uint8_t *rows = sh.tile[wave];
+    for (; tile < end; tile += kWaves) {
+      mask = mask_next;
+      // Scores of tokens 16 i + 4 h + e for head c.
+      f32x4 s[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        s[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int f = 0; f < kSteps; ++f) {
+          V k;
+          if constexpr (kI8)
+            k = f & 1 ? codes_f16(kr[i][f >> 1].z, kr[i][f >> 1].w)
+                      : codes_f16(kr[i][f >> 1].x, kr[i][f >> 1].y);
+          else
+            k = __builtin_bit_cast(V, kr[i][f]);
+#pragma unroll
+          for (int term = F::kTerms - 1; term >= 0; --term) s[i] = F::mfma(k, q[f][term], s[i]);
+        }
+      }
+      float vs[8];
+      if constexpr (kI8) {
+        if (h == 0) {
+          sh.scales[wave][0][c] = ksc[0];
+          sh.scales[wave][0][c + 16] = ksc[1];
+          sh.scales[wave][1][c] = vsc[0];
+          sh.scales[wave][1][c + 16] = vsc[1];
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const f32x4 ks4 = *reinterpret_cast<const f32x4 *>(&sh.scales[wave][0][16 * i + 4 * h]);
+          const f32x4 vs4 = *reinterpret_cast<const f32x4 *>(&sh.scales[wave][1][16 * i + 4 * h]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[i][e] *= ks4[e];
+            vs[4 * i + e] = vs4[e];
+          }
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+      const float vhere = kI8 ? fmaxf(vsc[0], vsc[1]) : 0.0f;
+
+      // The next tile's keys.
+      const bool all = mask == 0xffffffffu;
+      place(tile + kWaves);
+      load_pages(tile + 2 * kWaves);
+      load_rows(kbase, kr);
+
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[4 * i + e] = s[i][e] * unscale;
+          if (!all && !((mask >> (16 * i + 4 * h + e)) & 1)) x[4 * i + e] = -INFINITY;
+        }
+      float top = x[0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+      const float m_new = fmaxf(m, across4(top));
+      const float base = m_new == -INFINITY ? 0.0f : m_new;
+      float keep = exp2_fast(m - base);
+      if constexpr (kI8) {
+        const float v_new = fmaxf(vmax, pow2_above(wave_max(vhere)));
+        keep *= vmax * pow2_inverse(v_new);
+        vmax = v_new;
+      }
+      // l is not in units of vmax.
+      const float lkeep = kI8 ? exp2_fast(m - base) : keep;
+      m = m_new;
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = exp2_fast(x[e] - base + kUp);
+        sum += x[e];
+      }
+      l = l * lkeep + sum;
+      if constexpr (kI8) {
+        const float inv = pow2_inverse(vmax);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= vs[e] * inv;
+      }
+      if (__any(keep != 1.0f))
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) o[b] *= keep;
+      V p[F::kTerms];
+      F::split(x, p);
+
+      // Values: into LDS as rows, back as channels.
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool here = all || ((mask >> (c + 16 * i)) & 1);
+#pragma unroll
+        for (int pc = 0; pc < S::kPieces; ++pc) {
+          u32x4 v = vr[i][pc];
+          if (!here) v = u32x4{0u, 0u, 0u, 0u};
+          *reinterpret_cast<u32x4 *>(rows + (c + 16 * i) * S::kRow + 64 * pc + 16 * h) = v;
+        }
+      }
+      load_rows(vbase, vr);
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        V v;
+        if constexpr (kI8) {
+          const int row = 4 * h + (c >> 1 & 3) + 16 * (c >> 3);
+          typedef int v2i __attribute__((ext_vector_type(2)));
+          const v2i w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (BITNET_LDS v2i *)(rows + row * S::kRow + 16 * b + 8 * (c & 1)));
+          v = codes_f16((uint32_t)w.x, (uint32_t)w.y);
+        } else {
+          const uint8_t *at = rows + (4 * h + (c >> 2)) * S::kRow + 32 * b + 8 * (c & 3);
+          s16x4 w[2];
+          w[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((BITNET_LDS s16x4 *)at);
+          w[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((BITNET_LDS s16x4 *)(at + 16 * S::kRow));
+          v = __builtin_bit_cast(V, w);
+        }
+#pragma unroll
+        for (int term = F::kTerms - 1; term >= 0; --term) o[b] = F::mfma(v, p[term], o[b]);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
   }
-  part[tid] = o;
-  __syncthreads();
-  if (tid < D) {
-    for (int i = 1; i < kParts; ++i) o += part[tid + i * D];
-    a.out[((int64_t)t * a.q_heads + h) * D + tid] = l > 0.0f ? o / l : 0.0f;
+
+  // Join the waves: outputs 16 b + 4 h + e of head c, relative to the common
+  // maximum.
+  l = sum4(l);
+  if (h == 0) {
+    sh.m[wave][c] = m;
+    sh.l[wave][c] = l;
   }
-  if (tid == 0 && a.lse) a.lse[(int64_t)t * a.q_heads + h] = l > 0.0f ? m + logf(l) : -INFINITY;
+  __syncthreads();
+  float top = sh.m[0][c];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sh.m[w][c]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  const float mine = exp2_fast(m - base) * (kI8 ? vmax : 1.0f);
+  float *mo = reinterpret_cast<float *>(sh.tile[wave]);
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b)
+    *reinterpret_cast<f32x4 *>(mo + c * D + 16 * b + 4 * h) = o[b] * mine;
+  __syncthreads();
+  const int n4 = nh * D / 4;
+  uint8_t *ws = a.ws;
+  f32x2 *stats = reinterpret_cast<f32x2 *>(ws + stats_off) + (int64_t)item * parts * kHeads;
+  f32x4 *partial = reinterpret_cast<f32x4 *>(ws + kHeaderBytes) +
+                   (int64_t)item * parts * (kHeads * D / 4);
+  f32x4 *out = reinterpret_cast<f32x4 *>(a.out + ((int64_t)t * a.q_heads + head0) * D);
+  for (int i = threadIdx.x; i < n4; i += kThreads) {
+    f32x4 sum = reinterpret_cast<const f32x4 *>(sh.tile[0])[i];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) sum += reinterpret_cast<const f32x4 *>(sh.tile[w])[i];
+    const int head = i / (D / 4);
+    float tm = sh.m[0][head];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) tm = fmaxf(tm, sh.m[w][head]);
+    const float tb = tm == -INFINITY ? 0.0f : tm;
+    float tl = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) tl += sh.l[w][head] * exp2_fast(sh.m[w][head] - tb);
+    if (used == 1) {
+      out[i] = tl > 0.0f ? sum / tl : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (a.lse && i % (D / 4) == 0)
+        a.lse[(int64_t)t * a.q_heads + head0 + head] =
+            tl > 0.0f ? (tm - kUp + __log2f(tl)) * kLn2 : -INFINITY;
+    } else {
+      partial[part * (kHeads * D / 4) + i] = sum;
+      if (i % (D / 4) == 0) stats[part * kHeads + head] = f32x2{tm, tl};
+    }
+  }
+  if (used == 1) return;
+
+  // The last part to arrive joins them all; it leaves the counter at zero.
+  __threadfence();
+  __syncthreads();
+  uint32_t *ticket = reinterpret_cast<uint32_t *>(ws) + item;
+  if (threadIdx.x == 0) {
+    const uint32_t n = atomicAdd(ticket, 1u);
+    sh.last = n == (uint32_t)used - 1;
+    if (sh.last) atomicExch(ticket, 0u);
+  }
+  __syncthreads();
+  if (!sh.last) return;
+  __threadfence();
+  for (int i = threadIdx.x; i < n4; i += kThreads) {
+    const int head = i / (D / 4);
+    float tm = -INFINITY;
+    for (int p = 0; p < used; ++p) tm = fmaxf(tm, stats[p * kHeads + head].x);
+    const float tb = tm == -INFINITY ? 0.0f : tm;
+    float tl = 0.0f;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = 0; p < used; ++p) {
+      const f32x2 st = stats[p * kHeads + head];
+      const float w = exp2_fast(st.x - tb);
+      tl += st.y * w;
+      sum += partial[p * (kHeads * D / 4) + i] * w;
+    }
+    out[i] = tl > 0.0f ? sum / tl : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.lse && i % (D / 4) == 0)
+      a.lse[(int64_t)t * a.q_heads + head0 + head] =
+          tl > 0.0f ? (tm - kUp + __log2f(tl)) * kLn2 : -INFINITY;
+  }
 }
 
 template <int DT>
 void attend_dim(const AttendArgs &a, int D, hipStream_t stream) {
-  const dim3 grid(a.T, a.q_heads);
+  const AttendSplit s = attend_split(a.T, a.q_heads, a.c.kv_heads, D, a.max_len);
+  const unsigned grid = (unsigned)(s.items * s.parts);
   if (D == 64)
-    attend_kernel<DT, 64><<<grid, kThreads, 0, stream>>>(a);
+    attend_kernel<DT, 64><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
   else if (D == 128)
-    attend_kernel<DT, 128><<<grid, kThreads, 0, stream>>>(a);
+    attend_kernel<DT, 128><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
   else
-    attend_kernel<DT, 256><<<grid, kThreads, 0, stream>>>(a);
+    attend_kernel<DT, 256><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
 }
 
 }  // namespace
 
-size_t attend_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t) { return 16384; }
+size_t attend_workspace_bytes(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                              int64_t max_len) {
+  return attend_split(T, q_heads, kv_heads, head_dim, max_len).total;
+}
 
 hipError_t launch_attend(const AttendArgs &a, int dtype, int head_dim, hipStream_t stream) {
   if (dtype == BITNET_KV_BF16)

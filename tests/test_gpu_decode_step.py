@@ -12,9 +12,10 @@ add n u each, the exponentials, rescalings, joins and the division 64 u in all:
 8-bit rows add one rounding per scale (inside the 64).  A probability (relative
 to the row's largest, which is 1) below the smallest normal number of its format
 is lost: 2^-126 in fp32 and bf16; 2^-38 for fp16 values, whose probabilities are
-scaled by 2^14 against fp16's spacing of 2^-24.  Where the likely tokens' v are
-zero that is all that is left of an element: each token adds up to that much
-times max |v|."""
+scaled by 2^14 against fp16's spacing of 2^-24, and for 8-bit ones, whose
+probabilities carry their token's scale relative to a power of two at most twice
+the largest.  Where the likely tokens' v are zero that is all that is left of an
+element: each token adds up to that much times max |v|."""
 import sys
 
 import numpy as np
@@ -24,7 +25,7 @@ from oracle import decode_step as ref
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
-LOST = {"bf16": 2.0 ** -126, "fp16": 2.0 ** -38, "int8": 2.0 ** -126}
+LOST = {"bf16": 2.0 ** -126, "fp16": 2.0 ** -38, "int8": 2.0 ** -38}
 
 
 def say(msg):
@@ -379,6 +380,30 @@ def test_attention_large_scores(tb, dt):
     out, lse = tb.bitnet_paged_attention(tb.KvCache(*caches), 1, dev(q), dev(tables),
                                          dev(np.array(lens, np.int32)), scale=1.0, return_lse=True)
     check_attention(host(out), host(lse), q, ks, vs, 1.0, D, LOST[dt])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "int8"])
+def test_attention_small_values_and_uneven_channels(tb, dt):
+    """Keys and values down in fp16's subnormal numbers, queries with channels a
+    million times others, 8-bit scales that differ by many powers of two."""
+    say(f"[attend] small values {dt}")
+    lens, kv, G, D, ps = [130, 65], 2, 3, 128, 16
+    for spread, qs in ((2e-6, 1e6), (1.0, 1.0), (3e3, 1e-3)):
+        caches, tables, q, ks, vs = attend_inputs(8, lens, 12, kv, G, D, ps, dt, spread=spread)
+        q *= qs
+        q[:, ::7] *= 1e-6
+        if dt == "int8":
+            rng = np.random.default_rng(1)
+            for sc, vals in ((caches[2], ks), (caches[3], vs)):
+                f = np.exp2(rng.integers(-30, 1, tuple(sc.shape[1:]))).astype(np.float32)
+                sc[1] *= dev(f)
+                for r, n in enumerate(lens):
+                    j = np.arange(n)
+                    vals[r] *= f[tables[r, j // ps], :, j % ps].T[..., None]
+        out, lse = tb.bitnet_paged_attention(tb.KvCache(*caches), 1, dev(q), dev(tables),
+                                             dev(np.array(lens, np.int32)), scale=0.3,
+                                             return_lse=True)
+        check_attention(host(out), host(lse), q, ks, vs, 0.3, D, LOST[dt])
 
 
 def test_attention_rows_lens_and_bad_pages(tb):
