@@ -68,6 +68,20 @@ constexpr int kHeaderBytes = 4 * kTickets;
 constexpr int kMinTiles = 16;
 constexpr int kTargetGroups = 2048;
 constexpr int kMaxParts = 64;
+constexpr int kJoin = 8;          // parts whose results a joining thread has in flight
+
+// Partial results cross the chip through device-coherent accesses, eight bytes
+// each, so that no workgroup has to write back or invalidate a cache (a fence
+// of device scope does both).
+typedef unsigned long long u64;
+__device__ __forceinline__ void st_device(void *p, f32x2 v) {
+  __hip_atomic_store((BITNET_GLOBAL u64 *)p, __builtin_bit_cast(u64, v), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x2 ld_device(const void *p) {
+  return __builtin_bit_cast(f32x2, (u64)__hip_atomic_load((const BITNET_GLOBAL u64 *)p, __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT));
+}
 
 struct AttendSplit {
   int64_t items;
@@ -237,6 +251,7 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
       const int j = min(tile * kTile + c + 16 * i, len - 1);
       pg[i] = ld_global<int>(table + (j >> a.c.page_shift));
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   auto place = [&](int tile) {   // from pg: row offsets and mask of this tile
     uint32_t m[2];
@@ -261,6 +276,8 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int p = 0; p < S::kPieces; ++p) x[i][p] = ld_global<u32x4>(base + off[i] + 64 * p);
+    // Waits count loads in order of issue, so the groups stay in order.
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   float m = -INFINITY, l = 0.0f;
@@ -273,9 +290,9 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
   if (tile < end) {
     load_pages(tile);
     place(tile);
+    load_pages(tile + kWaves);
     load_rows(kbase, kr);
     load_rows(vbase, vr);
-    load_pages(tile + kWaves);
 
     // Queries as terms.
     V q[kSteps][F::kTerms];
@@ -452,17 +469,23 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
   for (int b = 0; b < kBlocks; ++b)
     *reinterpret_cast<f32x4 *>(mo + c * D + 16 * b + 4 * h) = o[b] * mine;
   __syncthreads();
-  const int n4 = nh * D / 4;
+  const int n2 = nh * D / 2;
   uint8_t *ws = a.ws;
   f32x2 *stats = reinterpret_cast<f32x2 *>(ws + stats_off) + (int64_t)item * parts * kHeads;
-  f32x4 *partial = reinterpret_cast<f32x4 *>(ws + kHeaderBytes) +
-                   (int64_t)item * parts * (kHeads * D / 4);
-  f32x4 *out = reinterpret_cast<f32x4 *>(a.out + ((int64_t)t * a.q_heads + head0) * D);
-  for (int i = threadIdx.x; i < n4; i += kThreads) {
-    f32x4 sum = reinterpret_cast<const f32x4 *>(sh.tile[0])[i];
+  f32x2 *partial = reinterpret_cast<f32x2 *>(ws + kHeaderBytes) +
+                   (int64_t)item * parts * (kHeads * D / 2);
+  f32x2 *out = reinterpret_cast<f32x2 *>(a.out + ((int64_t)t * a.q_heads + head0) * D);
+  auto finish = [&](int i, int head, f32x2 sum, float tm, float tl) {
+    out[i] = tl > 0.0f ? sum / tl : f32x2{0.0f, 0.0f};
+    if (a.lse && i % (D / 2) == 0)
+      a.lse[(int64_t)t * a.q_heads + head0 + head] =
+          tl > 0.0f ? (tm - kUp + __log2f(tl)) * kLn2 : -INFINITY;
+  };
+  for (int i = threadIdx.x; i < n2; i += kThreads) {
+    f32x2 sum = reinterpret_cast<const f32x2 *>(sh.tile[0])[i];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) sum += reinterpret_cast<const f32x4 *>(sh.tile[w])[i];
-    const int head = i / (D / 4);
+    for (int w = 1; w < kWaves; ++w) sum += reinterpret_cast<const f32x2 *>(sh.tile[w])[i];
+    const int head = i / (D / 2);
     float tm = sh.m[0][head];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) tm = fmaxf(tm, sh.m[w][head]);
@@ -471,46 +494,55 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) tl += sh.l[w][head] * exp2_fast(sh.m[w][head] - tb);
     if (used == 1) {
-      out[i] = tl > 0.0f ? sum / tl : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (a.lse && i % (D / 4) == 0)
-        a.lse[(int64_t)t * a.q_heads + head0 + head] =
-            tl > 0.0f ? (tm - kUp + __log2f(tl)) * kLn2 : -INFINITY;
+      finish(i, head, sum, tm, tl);
     } else {
-      partial[part * (kHeads * D / 4) + i] = sum;
-      if (i % (D / 4) == 0) stats[part * kHeads + head] = f32x2{tm, tl};
+      st_device(&partial[part * (kHeads * D / 2) + i], sum);
+      if (i % (D / 2) == 0) st_device(&stats[part * kHeads + head], f32x2{tm, tl});
     }
   }
   if (used == 1) return;
 
   // The last part to arrive joins them all; it leaves the counter at zero.
-  __threadfence();
+  // Each wave's stores have been acknowledged before the counter moves.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   uint32_t *ticket = reinterpret_cast<uint32_t *>(ws) + item;
   if (threadIdx.x == 0) {
-    const uint32_t n = atomicAdd(ticket, 1u);
+    const uint32_t n =
+        __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     sh.last = n == (uint32_t)used - 1;
-    if (sh.last) atomicExch(ticket, 0u);
+    if (sh.last) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
   if (!sh.last) return;
-  __threadfence();
-  for (int i = threadIdx.x; i < n4; i += kThreads) {
-    const int head = i / (D / 4);
-    float tm = -INFINITY;
-    for (int p = 0; p < used; ++p) tm = fmaxf(tm, stats[p * kHeads + head].x);
-    const float tb = tm == -INFINITY ? 0.0f : tm;
-    float tl = 0.0f;
-    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int p = 0; p < used; ++p) {
-      const f32x2 st = stats[p * kHeads + head];
-      const float w = exp2_fast(st.x - tb);
-      tl += st.y * w;
-      sum += partial[p * (kHeads * D / 4) + i] * w;
+  for (int i = threadIdx.x; i < n2; i += kThreads) {
+    const int head = i / (D / 2);
+    float tm = -INFINITY, tl = 0.0f;
+    f32x2 sum = {0.0f, 0.0f};
+    for (int p0 = 0; p0 < used; p0 += kJoin) {   // loads of kJoin parts at once
+      f32x2 st[kJoin], po[kJoin];
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) {
+        const int p = min(p0 + u, used - 1);
+        st[u] = ld_device(&stats[p * kHeads + head]);
+        po[u] = ld_device(&partial[p * (kHeads * D / 2) + i]);
+      }
+      float nm = tm;
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) nm = fmaxf(nm, st[u].x);
+      const float tb = nm == -INFINITY ? 0.0f : nm;
+      const float keep = exp2_fast(tm - tb);
+      tm = nm;
+      tl *= keep;
+      sum *= keep;
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) {
+        const float w = p0 + u < used ? exp2_fast(st[u].x - tb) : 0.0f;
+        tl += st[u].y * w;
+        sum += po[u] * w;
+      }
     }
-    out[i] = tl > 0.0f ? sum / tl : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (a.lse && i % (D / 4) == 0)
-      a.lse[(int64_t)t * a.q_heads + head0 + head] =
-          tl > 0.0f ? (tm - kUp + __log2f(tl)) * kLn2 : -INFINITY;
+    finish(i, head, sum, tm, tl);
   }
 }
 
