@@ -516,8 +516,9 @@ bitnet_status bitnet_ternary_matmul_stages(int64_t M, const bitnet_problem *prob
  *   limits       head_dim 64, 128 or 256; page_size a power of two, 1..1024;
  *                layers 1..1024, kv_heads 1..256, pages >= 1,
  *                pages * page_size < 2^31; k and v 16-byte aligned, strides
- *                multiples of 16 bytes, at least head_dim and below 2^40
- *                elements (layer_stride is not looked at when layers == 1).
+ *                multiples of 16 bytes, at least head_dim and below 2^31
+ *                elements (layer_stride below 2^40; it is not looked at when
+ *                layers == 1); fewer than 2^32 scales per layer.
  * The struct itself is host memory, read during the call.
  * ------------------------------------------------------------------------ */
 #define BITNET_KV_BF16 0

@@ -825,7 +825,7 @@ static int shift_of(int64_t v) {
   return s;
 }
 
-constexpr int64_t kMaxStride = (int64_t)1 << 40;   // of the cache, elements
+constexpr int64_t kMaxLayerStride = (int64_t)1 << 40;   // of the cache, elements
 constexpr int64_t kMaxTokens = kLimit / 256;       // rows of one call
 constexpr int64_t kMaxVocab = kLimit / 2;
 
@@ -842,13 +842,14 @@ static bitnet_status check_cache(const bitnet_kv_cache *c, int32_t layer) {
   if (c->kv_heads < 1 || c->kv_heads > 256 || c->pages < 1 ||
       (int64_t)c->pages * c->page_size >= kLimit)
     return BITNET_ERR_SHAPE;
+  if (i8 && (int64_t)c->pages * c->page_size * c->kv_heads >= 2 * kLimit) return BITNET_ERR_SHAPE;
   const int64_t per16 = i8 ? 16 : 8;   // elements in 16 bytes
-  const int64_t strides[4] = {c->page_stride, c->head_stride, c->token_stride,
-                              c->layers > 1 ? c->layer_stride : c->page_stride};
-  for (const int64_t s : strides) {
-    if (s < D || s >= kMaxStride) return BITNET_ERR_SHAPE;
-    if (s % per16 != 0) return BITNET_ERR_ALIGN;
-  }
+  const int64_t ls = c->layers > 1 ? c->layer_stride : c->page_stride;
+  for (const int64_t s : {c->page_stride, c->head_stride, c->token_stride})
+    if (s < D || s >= kLimit) return BITNET_ERR_SHAPE;
+  if (ls < D || ls >= kMaxLayerStride) return BITNET_ERR_SHAPE;
+  if (c->page_stride % per16 || c->head_stride % per16 || c->token_stride % per16 || ls % per16)
+    return BITNET_ERR_ALIGN;
   if (!aligned(c->k, 16) || !aligned(c->v, 16)) return BITNET_ERR_ALIGN;
   if (i8 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))) return BITNET_ERR_ALIGN;
   return BITNET_OK;

@@ -48,11 +48,15 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 #define BITNET_LDS __attribute__((address_space(3)))
 
-constexpr int kWaves = 4;
+#ifndef BITNET_ATTEND_WAVES
+#define BITNET_ATTEND_WAVES 4
+#endif
+constexpr int kWaves = BITNET_ATTEND_WAVES;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 32;         // tokens of a wave's step
 constexpr int kHeads = 16;        // query heads of a workgroup
@@ -65,8 +69,14 @@ constexpr int kHeaderBytes = 4 * kTickets;
 
 // How a call is cut: items = rows x key/value heads x groups of 16 query
 // heads, each in up to `parts` parts of at least kMinTiles tiles.
-constexpr int kMinTiles = 16;
-constexpr int kTargetGroups = 2048;
+#ifndef BITNET_ATTEND_MIN_TILES
+#define BITNET_ATTEND_MIN_TILES 16
+#endif
+#ifndef BITNET_ATTEND_GROUPS
+#define BITNET_ATTEND_GROUPS 2048
+#endif
+constexpr int kMinTiles = BITNET_ATTEND_MIN_TILES;
+constexpr int kTargetGroups = BITNET_ATTEND_GROUPS;
 constexpr int kMaxParts = 64;
 constexpr int kJoin = 8;          // parts whose results a joining thread has in flight
 
@@ -105,38 +115,65 @@ AttendSplit attend_split(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D
   return s;
 }
 
+// The operands of a type: products of 16 x 32 by 32 x 16, and fp32 values as
+// terms.  Folded (up to 8 heads), the 16 columns of an operand hold two terms
+// of 8 heads, the first in columns 0-7 and the second in columns 8-15: two
+// terms take one product, three take two.
 template <int DT> struct Frag;
 template <> struct Frag<BITNET_KV_BF16> {
   typedef bf16x8 V;
-  static constexpr int kTerms = 3, kBytes = 2;
+  static constexpr int kBytes = 2;
   static constexpr bool kHalf = false;
+  static constexpr int products(bool fold) { return fold ? 2 : 3; }
   static __device__ __forceinline__ f32x4 mfma(V a, V b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
-  static __device__ __forceinline__ void split(const float (&x)[8], V (&t)[kTerms]) {
+  template <bool FOLD>
+  static __device__ __forceinline__ void split(const float (&x)[8], bool second,
+                                               V (&t)[FOLD ? 2 : 3]) {
+    bf16x8 u[3];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float r = x[e];
+    for (int e = 0; e < 8; e += 2) {
+      f32x2 r = {x[e], x[e + 1]};
 #pragma unroll
-      for (int i = 0; i < kTerms; ++i) {
-        t[i][e] = (__bf16)r;
-        r -= (float)t[i][e];
+      for (int i = 0; i < 3; ++i) {
+        const bf16x2 b = __builtin_convertvector(r, bf16x2);
+        u[i][e] = b.x;
+        u[i][e + 1] = b.y;
+        r.x -= (float)b.x;
+        r.y -= (float)b.y;
       }
+    }
+    if constexpr (FOLD) {
+      t[0] = second ? u[1] : u[0];
+      t[1] = second ? bf16x8{} : u[2];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) t[i] = u[i];
     }
   }
 };
 struct FragF16 {
   typedef f16x8 V;
-  static constexpr int kTerms = 2;
   static constexpr bool kHalf = true;
+  static constexpr int products(bool fold) { return fold ? 1 : 2; }
   static __device__ __forceinline__ f32x4 mfma(V a, V b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
-  static __device__ __forceinline__ void split(const float (&x)[8], V (&t)[kTerms]) {
+  template <bool FOLD>
+  static __device__ __forceinline__ void split(const float (&x)[8], bool second,
+                                               V (&t)[FOLD ? 1 : 2]) {
+    f16x8 u[2];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      t[0][e] = (_Float16)x[e];
-      t[1][e] = (_Float16)(x[e] - (float)t[0][e]);
+      u[0][e] = (_Float16)x[e];
+      u[1][e] = (_Float16)(x[e] - (float)u[0][e]);
+    }
+    if constexpr (FOLD) {
+      t[0] = second ? u[1] : u[0];
+    } else {
+      t[0] = u[0];
+      t[1] = u[1];
     }
   }
 };
@@ -162,13 +199,26 @@ __device__ __forceinline__ f16x8 codes_f16(uint32_t lo, uint32_t hi) {
   return r;
 }
 
-__device__ __forceinline__ float across4(float v) {   // max over the lanes of one head
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
+// The lanes of one column are 16 apart.  The exchanges put rows 0, 2 (halves
+// 0) beside rows 1, 3 (halves 1), without leaving the registers.
+__device__ __forceinline__ float across4(float v) {   // maximum
+  const uint32_t a = __builtin_bit_cast(uint32_t, v);
+  const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const uint32_t p0 = p[0], p1 = p[1];   // (a bit cast of an element itself reads element 0)
+  const float m = fmaxf(__builtin_bit_cast(float, p0), __builtin_bit_cast(float, p1));
+  const uint32_t b = __builtin_bit_cast(uint32_t, m);
+  const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const uint32_t q0 = q[0], q1 = q[1];
+  return fmaxf(__builtin_bit_cast(float, q0), __builtin_bit_cast(float, q1));
 }
 __device__ __forceinline__ float sum4(float v) {
   v += __shfl_xor(v, 16, 64);
   return v + __shfl_xor(v, 32, 64);
+}
+// x plus x of the column eight further (row_ror:8).
+__device__ __forceinline__ float fold8(float x) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x128, 0xF, 0xF, false);
+  return x + __builtin_bit_cast(float, o);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -199,7 +249,7 @@ struct AttendShared {
   uint32_t last;
 };
 
-template <int DT, int D>
+template <int DT, int D, bool FOLD>
 __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
 attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
   typedef Frag<DT> F;
@@ -208,11 +258,14 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
   constexpr bool kI8 = DT == BITNET_KV_INT8;
   constexpr int kSteps = D / 32;       // contraction steps of the scores
   constexpr int kBlocks = D / 16;      // channel blocks of the outputs
+  constexpr int kProducts = F::products(FOLD);
   constexpr float kUp = F::kHalf ? 14.0f : 0.0f;   // probabilities are scaled by 2^kUp
   __shared__ AttendShared<DT, D> sh;
 
   const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool second = FOLD && c >= 8;
+  const int col = FOLD ? c & 7 : c;    // this lane's head
   const int per = a.q_heads / a.c.kv_heads;
   const int groups = (per + kHeads - 1) / kHeads;
   const int part = blockIdx.x % parts;
@@ -235,15 +288,15 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
   const uint8_t *kbase = reinterpret_cast<const uint8_t *>(a.c.k) + head_off;
   const uint8_t *vbase = reinterpret_cast<const uint8_t *>(a.c.v) + head_off;
   const int32_t *table = a.tables + (int64_t)max(min(r, a.table_rows - 1), 0) * a.max_pages;
-  const int64_t page_bytes = a.c.page_stride * S::kBytes;
+  const uint32_t page_bytes = (uint32_t)(a.c.page_stride * S::kBytes);
+  const uint32_t tok_bytes = (uint32_t)(a.c.token_stride * S::kBytes);
   const int tok_mask = (1 << a.c.page_shift) - 1;
-  const int64_t tok_bytes = a.c.token_stride * S::kBytes;
 
   int pg[2];                       // pages of tokens c, c + 16 of the tile after the loaded one
   u32x4 kr[2][S::kPieces], vr[2][S::kPieces];
   float ksc[2], vsc[2];
-  uint32_t mask, mask_next;        // tokens of the tile that are there
-  int64_t off[2];
+  uint32_t mask_next;              // tokens of the loaded tile that are there
+  uint64_t off[2];
 
   auto load_pages = [&](int tile) {
 #pragma unroll
@@ -259,10 +312,10 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
     for (int i = 0; i < 2; ++i) {
       const int j = tile * kTile + c + 16 * i;
       const bool ok = tile < end && j < len && (uint32_t)pg[i] < (uint32_t)a.c.pages;
-      const int page = ok ? pg[i] : 0, tok = ok ? j & tok_mask : 0;
-      off[i] = page * page_bytes + tok * tok_bytes;
+      const uint32_t page = ok ? pg[i] : 0, tok = ok ? j & tok_mask : 0;
+      off[i] = (uint64_t)page * page_bytes + (uint64_t)tok * tok_bytes;
       if constexpr (kI8) {
-        const int64_t at = (((int64_t)page * a.c.kv_heads + kvh) << a.c.page_shift) + tok;
+        const uint32_t at = ((page * (uint32_t)a.c.kv_heads + kvh) << a.c.page_shift) + tok;
         const float ks = ld_global<float>(a.c.k_scale + at), vs = ld_global<float>(a.c.v_scale + at);
         ksc[i] = ok ? ks : 0.0f;
         vsc[i] = ok ? vs : 0.0f;
@@ -270,6 +323,7 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
       m[i] = (uint32_t)__ballot(ok) & 0xffffu;
     }
     mask_next = m[0] | (m[1] << 16);
+    __builtin_amdgcn_sched_barrier(0);
   };
   auto load_rows = [&](const uint8_t *base, u32x4 (&x)[2][S::kPieces]) {
 #pragma unroll
@@ -291,14 +345,14 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
     load_pages(tile);
     place(tile);
     load_pages(tile + kWaves);
-    load_rows(kbase, kr);
     load_rows(vbase, vr);
+    load_rows(kbase, kr);
 
     // Queries as terms.
-    V q[kSteps][F::kTerms];
+    V q[kSteps][kProducts];
     float unscale = 1.0f;
     {
-      const float *src = a.q + t * a.q_stride + (int64_t)(head0 + min(c, nh - 1)) * D;
+      const float *src = a.q + t * a.q_stride + (int64_t)(head0 + min(col, nh - 1)) * D;
       float x[kSteps][8];
       float big = 0.0f;
 #pragma unroll
@@ -322,31 +376,26 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
       for (int f = 0; f < kSteps; ++f) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[f][e] *= up;
-        F::split(x[f], q[f]);
+        F::template split<FOLD>(x[f], second, q[f]);
       }
     }
 
     uint8_t *rows = sh.tile[wave];
     for (; tile < end; tile += kWaves) {
-      mask = mask_next;
-      // Scores of tokens 16 i + 4 h + e for head c.
-      f32x4 s[2];
+      const uint32_t mask = mask_next;
+      const bool all = mask == 0xffffffffu;
+      // Values into LDS, as rows; scales too.
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        s[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const bool here = all || ((mask >> (c + 16 * i)) & 1);
 #pragma unroll
-        for (int f = 0; f < kSteps; ++f) {
-          V k;
-          if constexpr (kI8)
-            k = f & 1 ? codes_f16(kr[i][f >> 1].z, kr[i][f >> 1].w)
-                      : codes_f16(kr[i][f >> 1].x, kr[i][f >> 1].y);
-          else
-            k = __builtin_bit_cast(V, kr[i][f]);
-#pragma unroll
-          for (int term = F::kTerms - 1; term >= 0; --term) s[i] = F::mfma(k, q[f][term], s[i]);
+        for (int pc = 0; pc < S::kPieces; ++pc) {
+          u32x4 v = vr[i][pc];
+          if (!here) v = u32x4{0u, 0u, 0u, 0u};
+          *reinterpret_cast<u32x4 *>(rows + (c + 16 * i) * S::kRow + 64 * pc + 16 * h) = v;
         }
       }
-      float vs[8];
+      float ks[8], vs[8];
       if constexpr (kI8) {
         if (h == 0) {
           sh.scales[wave][0][c] = ksc[0];
@@ -361,18 +410,37 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
           const f32x4 vs4 = *reinterpret_cast<const f32x4 *>(&sh.scales[wave][1][16 * i + 4 * h]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[i][e] *= ks4[e];
+            ks[4 * i + e] = ks4[e] * unscale;
             vs[4 * i + e] = vs4[e];
           }
         }
-        __builtin_amdgcn_wave_barrier();
       }
-      const float vhere = kI8 ? fmaxf(vsc[0], vsc[1]) : 0.0f;
-
-      // The next tile's keys.
-      const bool all = mask == 0xffffffffu;
+      // The next tile's values.
       place(tile + kWaves);
       load_pages(tile + 2 * kWaves);
+      load_rows(vbase, vr);
+
+      // Scores of tokens 16 i + 4 h + e for this column.
+      f32x4 s[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) s[i][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int f = 0; f < kSteps; ++f)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          V k;
+          if constexpr (kI8)
+            k = f & 1 ? codes_f16(kr[i][f >> 1].z, kr[i][f >> 1].w)
+                      : codes_f16(kr[i][f >> 1].x, kr[i][f >> 1].y);
+          else
+            k = __builtin_bit_cast(V, kr[i][f]);
+#pragma unroll
+          for (int p = kProducts - 1; p >= 0; --p) s[i][f & 1] = F::mfma(k, q[f][p], s[i][f & 1]);
+        }
+      // The next tile's keys.
+      __builtin_amdgcn_sched_barrier(0);
       load_rows(kbase, kr);
 
       float x[8];
@@ -380,53 +448,52 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[4 * i + e] = s[i][e] * unscale;
-          if (!all && !((mask >> (16 * i + 4 * h + e)) & 1)) x[4 * i + e] = -INFINITY;
+          float y = s[i][0][e] + s[i][1][e];
+          if constexpr (FOLD) y = fold8(y);
+          y *= kI8 ? ks[4 * i + e] : unscale;
+          x[4 * i + e] = y;
         }
+      if (!all)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!((mask >> (16 * i + 4 * h + e)) & 1)) x[4 * i + e] = -INFINITY;
       float top = x[0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
       const float m_new = fmaxf(m, across4(top));
       const float base = m_new == -INFINITY ? 0.0f : m_new;
-      float keep = exp2_fast(m - base);
+      const float lkeep = exp2_fast(m - base);
+      float keep = lkeep;
+      float inv = 1.0f;
       if constexpr (kI8) {
-        const float v_new = fmaxf(vmax, pow2_above(wave_max(vhere)));
-        keep *= vmax * pow2_inverse(v_new);
+        float vt = vs[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) vt = fmaxf(vt, vs[e]);
+        const float v_new = fmaxf(vmax, pow2_above(across4(vt)));
+        inv = pow2_inverse(v_new);
+        keep *= vmax * inv;
         vmax = v_new;
       }
-      // l is not in units of vmax.
-      const float lkeep = kI8 ? exp2_fast(m - base) : keep;
       m = m_new;
       float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] = exp2_fast(x[e] - base + kUp);
+        x[e] = exp2_fast(x[e] - (base - kUp));
         sum += x[e];
       }
-      l = l * lkeep + sum;
-      if constexpr (kI8) {
-        const float inv = pow2_inverse(vmax);
+      l = l * lkeep + sum;   // not in units of vmax
+      if constexpr (kI8)
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] *= vs[e] * inv;
-      }
       if (__any(keep != 1.0f))
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) o[b] *= keep;
-      V p[F::kTerms];
-      F::split(x, p);
+      V p[kProducts];
+      F::template split<FOLD>(x, second, p);
 
-      // Values: into LDS as rows, back as channels.
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bool here = all || ((mask >> (c + 16 * i)) & 1);
-#pragma unroll
-        for (int pc = 0; pc < S::kPieces; ++pc) {
-          u32x4 v = vr[i][pc];
-          if (!here) v = u32x4{0u, 0u, 0u, 0u};
-          *reinterpret_cast<u32x4 *>(rows + (c + 16 * i) * S::kRow + 64 * pc + 16 * h) = v;
-        }
-      }
-      load_rows(vbase, vr);
+      // Values back from LDS, four tokens of a channel at a time.
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
@@ -445,17 +512,22 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
           v = __builtin_bit_cast(V, w);
         }
 #pragma unroll
-        for (int term = F::kTerms - 1; term >= 0; --term) o[b] = F::mfma(v, p[term], o[b]);
+        for (int i = kProducts - 1; i >= 0; --i) o[b] = F::mfma(v, p[i], o[b]);
       }
       __builtin_amdgcn_wave_barrier();
     }
+    if constexpr (FOLD)
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[b][e] = fold8(o[b][e]);
   }
 
   // Join the waves: outputs 16 b + 4 h + e of head c, relative to the common
   // maximum.
   l = sum4(l);
   if (h == 0) {
-    sh.m[wave][c] = m;
+    sh.m[wave][c] = m;   // folded: columns 8-15 repeat heads 0-7 and are not read
     sh.l[wave][c] = l;
   }
   __syncthreads();
@@ -467,7 +539,7 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
   float *mo = reinterpret_cast<float *>(sh.tile[wave]);
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b)
-    *reinterpret_cast<f32x4 *>(mo + c * D + 16 * b + 4 * h) = o[b] * mine;
+    if (!second) *reinterpret_cast<f32x4 *>(mo + c * D + 16 * b + 4 * h) = o[b] * mine;
   __syncthreads();
   const int n2 = nh * D / 2;
   uint8_t *ws = a.ws;
@@ -546,16 +618,24 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
   }
 }
 
-template <int DT>
+template <int DT, bool FOLD>
 void attend_dim(const AttendArgs &a, int D, hipStream_t stream) {
   const AttendSplit s = attend_split(a.T, a.q_heads, a.c.kv_heads, D, a.max_len);
   const unsigned grid = (unsigned)(s.items * s.parts);
   if (D == 64)
-    attend_kernel<DT, 64><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
+    attend_kernel<DT, 64, FOLD><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
   else if (D == 128)
-    attend_kernel<DT, 128><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
+    attend_kernel<DT, 128, FOLD><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
   else
-    attend_kernel<DT, 256><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
+    attend_kernel<DT, 256, FOLD><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
+}
+
+template <int DT>
+void attend_type(const AttendArgs &a, int D, hipStream_t stream) {
+  if (a.q_heads <= 8 * a.c.kv_heads)
+    attend_dim<DT, true>(a, D, stream);
+  else
+    attend_dim<DT, false>(a, D, stream);
 }
 
 }  // namespace
@@ -567,11 +647,11 @@ size_t attend_workspace_bytes(int64_t T, int64_t q_heads, int64_t kv_heads, int6
 
 hipError_t launch_attend(const AttendArgs &a, int dtype, int head_dim, hipStream_t stream) {
   if (dtype == BITNET_KV_BF16)
-    attend_dim<BITNET_KV_BF16>(a, head_dim, stream);
+    attend_type<BITNET_KV_BF16>(a, head_dim, stream);
   else if (dtype == BITNET_KV_FP16)
-    attend_dim<BITNET_KV_FP16>(a, head_dim, stream);
+    attend_type<BITNET_KV_FP16>(a, head_dim, stream);
   else
-    attend_dim<BITNET_KV_INT8>(a, head_dim, stream);
+    attend_type<BITNET_KV_INT8>(a, head_dim, stream);
   return hipGetLastError();
 }
 

@@ -32,7 +32,9 @@ BAD_CACHES = [
     (dict(dtype=-1), SHAPE), (dict(head_dim=96), SHAPE), (dict(page_size=48), SHAPE),
     (dict(page_size=0), SHAPE), (dict(page_size=2048), SHAPE), (dict(layers=0), SHAPE),
     (dict(kv_heads=0), SHAPE), (dict(kv_heads=257), SHAPE), (dict(pages=0), SHAPE),
-    (dict(pages=1 << 25), SHAPE), (dict(token_stride=64), SHAPE), (dict(head_stride=1 << 40), SHAPE),
+    (dict(pages=1 << 25), SHAPE), (dict(token_stride=64), SHAPE), (dict(head_stride=1 << 31), SHAPE),
+    (dict(layer_stride=1 << 40), SHAPE),
+    (dict(dtype=2, k_scale=A, v_scale=A, kv_heads=256, pages=1 << 24), SHAPE),
     (dict(page_stride=(1 << 14) + 4), ALIGN), (dict(layer_stride=4), SHAPE),
     (dict(k=A + 8), ALIGN), (dict(dtype=2, k_scale=A + 2, v_scale=A), ALIGN),
     (dict(dtype=2, k_scale=A, v_scale=A, token_stride=136), ALIGN),
