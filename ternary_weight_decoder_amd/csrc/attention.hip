@@ -78,19 +78,17 @@ constexpr int kHeaderBytes = 4 * kTickets;
 constexpr int kMinTiles = BITNET_ATTEND_MIN_TILES;
 constexpr int kTargetGroups = BITNET_ATTEND_GROUPS;
 constexpr int kMaxParts = 64;
-constexpr int kJoin = 8;          // parts whose results a joining thread has in flight
 
-// Partial results cross the chip through device-coherent accesses, eight bytes
-// each, so that no workgroup has to write back or invalidate a cache (a fence
-// of device scope does both).
-typedef unsigned long long u64;
-__device__ __forceinline__ void st_device(void *p, f32x2 v) {
-  __hip_atomic_store((BITNET_GLOBAL u64 *)p, __builtin_bit_cast(u64, v), __ATOMIC_RELAXED,
-                     __HIP_MEMORY_SCOPE_AGENT);
+// Partial results cross the chip through device-coherent accesses (cache
+// policy sc1), so that no workgroup has to write back or invalidate a cache,
+// as a fence of device scope does.
+constexpr int kDeviceAux = 16;
+__device__ __forceinline__ void st_device(__amdgpu_buffer_rsrc_t rsrc, uint32_t off, f32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, off, 0, kDeviceAux);
 }
-__device__ __forceinline__ f32x2 ld_device(const void *p) {
-  return __builtin_bit_cast(f32x2, (u64)__hip_atomic_load((const BITNET_GLOBAL u64 *)p, __ATOMIC_RELAXED,
-                                                     __HIP_MEMORY_SCOPE_AGENT));
+__device__ __forceinline__ f32x4 ld_device(__amdgpu_buffer_rsrc_t rsrc, uint32_t off) {
+  return __builtin_bit_cast(f32x4,
+                            __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, kDeviceAux));
 }
 
 struct AttendSplit {
@@ -212,8 +210,28 @@ __device__ __forceinline__ float across4(float v) {   // maximum
   return fmaxf(__builtin_bit_cast(float, q0), __builtin_bit_cast(float, q1));
 }
 __device__ __forceinline__ float sum4(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
+  const uint32_t a = __builtin_bit_cast(uint32_t, v);
+  const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const uint32_t p0 = p[0], p1 = p[1];
+  const float m = __builtin_bit_cast(float, p0) + __builtin_bit_cast(float, p1);
+  const uint32_t b = __builtin_bit_cast(uint32_t, m);
+  const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const uint32_t q0 = q[0], q1 = q[1];
+  return __builtin_bit_cast(float, q0) + __builtin_bit_cast(float, q1);
+}
+// Maximum or sum over the 16 lanes of a row: quads, then mirrored halves.
+template <int CTRL, bool MAX>
+__device__ __forceinline__ float row_step(float v) {
+  const float o = __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+  return MAX ? fmaxf(v, o) : v + o;
+}
+template <bool MAX>
+__device__ __forceinline__ float across16(float v) {
+  v = row_step<0xB1, MAX>(v);    // quad_perm 1,0,3,2
+  v = row_step<0x4E, MAX>(v);    // quad_perm 2,3,0,1
+  v = row_step<0x141, MAX>(v);   // row_half_mirror
+  return row_step<0x140, MAX>(v);   // row_mirror
 }
 // x plus x of the column eight further (row_ror:8).
 __device__ __forceinline__ float fold8(float x) {
@@ -245,7 +263,8 @@ template <int DT, int D>
 struct AttendShared {
   __attribute__((aligned(16))) uint8_t tile[kWaves][Shape<DT, D>::kWaveLds];
   float scales[kWaves][2][kTile];      // 8-bit caches: the tile's key and value scales
-  float m[kWaves][kHeads], l[kWaves][kHeads];
+  float m[kWaves][kHeads], l[kWaves][kHeads], unit[kWaves];
+  float weight[kHeads][kMaxParts];     // of the joined parts
   uint32_t last;
 };
 
@@ -268,12 +287,25 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
   const int col = FOLD ? c & 7 : c;    // this lane's head
   const int per = a.q_heads / a.c.kv_heads;
   const int groups = (per + kHeads - 1) / kHeads;
-  const int part = blockIdx.x % parts;
-  const int item = blockIdx.x / parts;
+  const int part = parts > 1 ? blockIdx.x : 0;
+  const int item = parts > 1 ? blockIdx.y : blockIdx.x;
   const int t = item / (a.c.kv_heads * groups);
   const int kvh = item / groups % a.c.kv_heads;
   const int head0 = kvh * per + item % groups * kHeads;   // first query head
   const int nh = min(kHeads, per - item % groups * kHeads);
+
+  // The queries: asked for first, used once the first rows are on their way.
+  f32x4 qx[kSteps][2];
+  {
+    const float *src = a.q + t * a.q_stride + (int64_t)(head0 + min(col, nh - 1)) * D;
+#pragma unroll
+    for (int f = 0; f < kSteps; ++f) {
+      const int d = kI8 ? (f >> 1) * 64 + 16 * h + (f & 1) * 8 : f * 32 + 8 * h;
+      qx[f][0] = ld_global<f32x4>(src + d);
+      qx[f][1] = ld_global<f32x4>(src + d + 4);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
 
   const int r = a.rows ? a.rows[t] : t;
   const int len = r >= 0 && r < a.table_rows ? min(max(a.lens[t], 0), a.max_len) : 0;
@@ -352,20 +384,15 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
     V q[kSteps][kProducts];
     float unscale = 1.0f;
     {
-      const float *src = a.q + t * a.q_stride + (int64_t)(head0 + min(col, nh - 1)) * D;
       float x[kSteps][8];
       float big = 0.0f;
 #pragma unroll
-      for (int f = 0; f < kSteps; ++f) {
-        const int d = kI8 ? (f >> 1) * 64 + 16 * h + (f & 1) * 8 : f * 32 + 8 * h;
-        const f32x4 lo = ld_global<f32x4>(src + d), hi = ld_global<f32x4>(src + d + 4);
+      for (int f = 0; f < kSteps; ++f)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[f][e] = lo[e] * (a.scale * kLog2e);
-          x[f][e + 4] = hi[e] * (a.scale * kLog2e);
-          big = fmaxf(big, fmaxf(fabsf(x[f][e]), fabsf(x[f][e + 4])));
+        for (int e = 0; e < 8; ++e) {
+          x[f][e] = qx[f][e >> 2][e & 3] * (a.scale * kLog2e);
+          big = fmaxf(big, fabsf(x[f][e]));
         }
-      }
       float up = 1.0f;
       if constexpr (F::kHalf) {
         const float p2 = pow2_above(across4(big));
@@ -523,53 +550,55 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
         for (int e = 0; e < 4; ++e) o[b][e] = fold8(o[b][e]);
   }
 
-  // Join the waves: outputs 16 b + 4 h + e of head c, relative to the common
-  // maximum.
+  // Join the waves: outputs 16 b + 4 h + e of head c, each wave's relative to
+  // its own maximum (folded: columns 8-15 repeat heads 0-7 and are left out).
   l = sum4(l);
   if (h == 0) {
-    sh.m[wave][c] = m;   // folded: columns 8-15 repeat heads 0-7 and are not read
+    sh.m[wave][c] = m;
     sh.l[wave][c] = l;
   }
-  __syncthreads();
-  float top = sh.m[0][c];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sh.m[w][c]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  const float mine = exp2_fast(m - base) * (kI8 ? vmax : 1.0f);
-  float *mo = reinterpret_cast<float *>(sh.tile[wave]);
+  if (lane == 0) sh.unit[wave] = vmax;
+  f32x4 *mine = reinterpret_cast<f32x4 *>(sh.tile[wave]);
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b)
-    if (!second) *reinterpret_cast<f32x4 *>(mo + c * D + 16 * b + 4 * h) = o[b] * mine;
+    if (!second) mine[c * (D / 4) + 4 * b + h] = o[b];
   __syncthreads();
-  const int n2 = nh * D / 2;
-  uint8_t *ws = a.ws;
-  f32x2 *stats = reinterpret_cast<f32x2 *>(ws + stats_off) + (int64_t)item * parts * kHeads;
-  f32x2 *partial = reinterpret_cast<f32x2 *>(ws + kHeaderBytes) +
-                   (int64_t)item * parts * (kHeads * D / 2);
-  f32x2 *out = reinterpret_cast<f32x2 *>(a.out + ((int64_t)t * a.q_heads + head0) * D);
-  auto finish = [&](int i, int head, f32x2 sum, float tm, float tl) {
-    out[i] = tl > 0.0f ? sum / tl : f32x2{0.0f, 0.0f};
-    if (a.lse && i % (D / 2) == 0)
+  constexpr int kQuads = D / 4;        // of a head
+  const int n4 = nh * kQuads;
+  // Workspace of this item: outputs [parts][kHeads][D], (max, sum) [parts][kHeads].
+  const uint32_t part_bytes = kHeads * D * 4;
+  const __amdgpu_buffer_rsrc_t outs =
+      make_rsrc(a.ws + kHeaderBytes + (int64_t)item * parts * part_bytes, parts * part_bytes);
+  f32x2 *stats = reinterpret_cast<f32x2 *>(a.ws + stats_off) + (int64_t)item * parts * kHeads;
+  f32x4 *out = reinterpret_cast<f32x4 *>(a.out + ((int64_t)t * a.q_heads + head0) * D);
+  auto finish = [&](int i, int head, f32x4 sum, float tm, float tl) {
+    st_global<f32x4>(out + i, tl > 0.0f ? sum / tl : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+    if (a.lse && i % kQuads == 0)
       a.lse[(int64_t)t * a.q_heads + head0 + head] =
           tl > 0.0f ? (tm - kUp + __log2f(tl)) * kLn2 : -INFINITY;
   };
-  for (int i = threadIdx.x; i < n2; i += kThreads) {
-    f32x2 sum = reinterpret_cast<const f32x2 *>(sh.tile[0])[i];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) sum += reinterpret_cast<const f32x2 *>(sh.tile[w])[i];
-    const int head = i / (D / 2);
+  for (int i = threadIdx.x; i < n4; i += kThreads) {
+    const int head = i / kQuads;
     float tm = sh.m[0][head];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) tm = fmaxf(tm, sh.m[w][head]);
-    const float tb = tm == -INFINITY ? 0.0f : tm;
+    const float base = tm == -INFINITY ? 0.0f : tm;
     float tl = 0.0f;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) tl += sh.l[w][head] * exp2_fast(sh.m[w][head] - tb);
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = exp2_fast(sh.m[w][head] - base);
+      tl += sh.l[w][head] * f;
+      sum += reinterpret_cast<const f32x4 *>(sh.tile[w])[i] * (kI8 ? f * sh.unit[w] : f);
+    }
     if (used == 1) {
       finish(i, head, sum, tm, tl);
     } else {
-      st_device(&partial[part * (kHeads * D / 2) + i], sum);
-      if (i % (D / 2) == 0) st_device(&stats[part * kHeads + head], f32x2{tm, tl});
+      st_device(outs, part * part_bytes + 16 * i, sum);
+      if (i % kQuads == 0)
+        __hip_atomic_store((BITNET_GLOBAL uint64_t *)&stats[part * kHeads + head],
+                           __builtin_bit_cast(uint64_t, f32x2{tm, tl}), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
     }
   }
   if (used == 1) return;
@@ -578,8 +607,8 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
   // Each wave's stores have been acknowledged before the counter moves.
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  uint32_t *ticket = reinterpret_cast<uint32_t *>(ws) + item;
   if (threadIdx.x == 0) {
+    uint32_t *ticket = reinterpret_cast<uint32_t *>(a.ws) + item;
     const uint32_t n =
         __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     sh.last = n == (uint32_t)used - 1;
@@ -587,41 +616,65 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
   }
   __syncthreads();
   if (!sh.last) return;
-  for (int i = threadIdx.x; i < n2; i += kThreads) {
-    const int head = i / (D / 2);
-    float tm = -INFINITY, tl = 0.0f;
-    f32x2 sum = {0.0f, 0.0f};
-    for (int p0 = 0; p0 < used; p0 += kJoin) {   // loads of kJoin parts at once
-      f32x2 st[kJoin], po[kJoin];
+  // Wave w adds up parts w, w + kWaves, ..., a lane per four channels in each
+  // of kWide stretches of the outputs; the loads of kJoin parts go out at once,
+  // the first ones before the weights are known.
+  constexpr int kWide = (FOLD ? 8 : kHeads) * kQuads / 64;
+  constexpr int kJoin = kWide >= 8 ? 2 : 16 / kWide;
+  f32x4 x[kJoin][kWide], sum[kWide];
+  auto load_parts = [&](int p0) {
 #pragma unroll
-      for (int u = 0; u < kJoin; ++u) {
-        const int p = min(p0 + u, used - 1);
-        st[u] = ld_device(&stats[p * kHeads + head]);
-        po[u] = ld_device(&partial[p * (kHeads * D / 2) + i]);
-      }
-      float nm = tm;
+    for (int u = 0; u < kJoin; ++u)
 #pragma unroll
-      for (int u = 0; u < kJoin; ++u) nm = fmaxf(nm, st[u].x);
-      const float tb = nm == -INFINITY ? 0.0f : nm;
-      const float keep = exp2_fast(tm - tb);
-      tm = nm;
-      tl *= keep;
-      sum *= keep;
-#pragma unroll
-      for (int u = 0; u < kJoin; ++u) {
-        const float w = p0 + u < used ? exp2_fast(st[u].x - tb) : 0.0f;
-        tl += st[u].y * w;
-        sum += po[u] * w;
-      }
+      for (int b = 0; b < kWide; ++b)
+        x[u][b] = ld_device(outs, min(p0 + u * kWaves, used - 1) * part_bytes +
+                                      16 * min(64 * b + lane, n4 - 1));
+  };
+  load_parts(wave);
+  // A wave per head turns the parts' maxima and sums into weights.
+  for (int head = wave; head < nh; head += kWaves) {
+    f32x2 st = {-INFINITY, 0.0f};
+    if (lane < used)
+      st = __builtin_bit_cast(f32x2, (uint64_t)__hip_atomic_load(
+                                         (const BITNET_GLOBAL uint64_t *)&stats[lane * kHeads + head],
+                                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    const float tm = across16<true>(across4(st.x));
+    const float f = exp2_fast(st.x - (tm == -INFINITY ? 0.0f : tm));
+    const float tl = across16<false>(sum4(st.y * f));
+    if (lane < used) sh.weight[head][lane] = f;
+    if (lane == 0) {
+      sh.m[0][head] = tm;
+      sh.l[0][head] = tl;
     }
-    finish(i, head, sum, tm, tl);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < kWide; ++b) sum[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int p0 = wave; p0 < used; p0 += kJoin * kWaves) {
+    if (p0 != wave) load_parts(p0);
+#pragma unroll
+    for (int u = 0; u < kJoin; ++u)
+      if (p0 + u * kWaves < used)
+#pragma unroll
+        for (int b = 0; b < kWide; ++b)
+          sum[b] += x[u][b] * sh.weight[min(64 * b + lane, n4 - 1) / kQuads][p0 + u * kWaves];
+  }
+#pragma unroll
+  for (int b = 0; b < kWide; ++b)
+    if (64 * b + lane < n4) mine[64 * b + lane] = sum[b];
+  __syncthreads();
+  for (int i = threadIdx.x; i < n4; i += kThreads) {
+    f32x4 sum = reinterpret_cast<const f32x4 *>(sh.tile[0])[i];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) sum += reinterpret_cast<const f32x4 *>(sh.tile[w])[i];
+    finish(i, i / kQuads, sum, sh.m[0][i / kQuads], sh.l[0][i / kQuads]);
   }
 }
 
 template <int DT, bool FOLD>
 void attend_dim(const AttendArgs &a, int D, hipStream_t stream) {
   const AttendSplit s = attend_split(a.T, a.q_heads, a.c.kv_heads, D, a.max_len);
-  const unsigned grid = (unsigned)(s.items * s.parts);
+  const dim3 grid = s.parts > 1 ? dim3(s.parts, s.items) : dim3(s.items);
   if (D == 64)
     attend_kernel<DT, 64, FOLD><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
   else if (D == 128)
