@@ -6,8 +6,8 @@
 // stream of key and value rows.  A workgroup takes one row t, one key/value
 // head with up to 16 of its query heads, and a part of the row's length; its
 // waves walk 32-token tiles, each with its own running maximum, sum and
-// outputs, and join them in LDS at the end.  Parts of a long row are joined by
-// the workgroup that finishes last.
+// outputs, and join them in LDS at the end.  Parts of a row are joined by the
+// workgroup that finishes last.
 //
 // Tile.  Lane L = c + 16h loads, for tokens c and c + 16, the 16-byte pieces
 // h, h + 4, ... of the key row and of the value row: keys and values lie at
@@ -29,12 +29,11 @@
 // do by powers of two: queries by their head's largest channel, probabilities
 // by 2^14, and with 8-bit values by the largest value scale so far.
 //
-// While a tile is worked on, the next one's rows are in flight: its keys are
-// asked for once the scores are done with the registers, its values once
-// they are in LDS, its pages a tile earlier.  All loads are unconditional, so
-// that the waits count exactly: a token that is not there (behind the length,
-// or on a page out of range) reads row 0 of page 0 instead; its score becomes
-// -inf and its value zero, whatever memory holds.
+// While a tile's softmax and outputs are worked on, the next one's rows are in
+// flight: asked for once the scores are done with the keys' registers and the
+// values are in LDS, their pages a tile earlier.  A token that is not there
+// (behind the length, or on a page out of range) reads row 0 of page 0
+// instead; its score becomes -inf and its value zero, whatever memory holds.
 #include <algorithm>
 
 #include "bitnet_device.hpp"
@@ -53,31 +52,36 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 #define BITNET_LDS __attribute__((address_space(3)))
 
-#ifndef BITNET_ATTEND_WAVES
-#define BITNET_ATTEND_WAVES 4
-#endif
-constexpr int kWaves = BITNET_ATTEND_WAVES;
+constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 32;         // tokens of a wave's step
 constexpr int kHeads = 16;        // query heads of a workgroup
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Tickets of the parts' joins: one counter per (row, head) pair that is split.
-constexpr int kTickets = 4096;
-constexpr int kHeaderBytes = 4 * kTickets;
-
-// How a call is cut: items = rows x key/value heads x groups of 16 query
-// heads, each in up to `parts` parts of at least kMinTiles tiles.
-#ifndef BITNET_ATTEND_MIN_TILES
-#define BITNET_ATTEND_MIN_TILES 16
-#endif
-#ifndef BITNET_ATTEND_GROUPS
-#define BITNET_ATTEND_GROUPS 2048
-#endif
-constexpr int kMinTiles = BITNET_ATTEND_MIN_TILES;
-constexpr int kTargetGroups = BITNET_ATTEND_GROUPS;
-constexpr int kMaxParts = 64;
+// Work.  An item is one row, one key/value head and one group of up to 16 of
+// its query heads.  Its tiles follow each other, and the items each other, in
+// one line, which is cut into equal stretches, a workgroup each, from the
+// lengths on the device.
+//   - Much work: stretches of total / grid tiles, so that ragged rows keep no
+//     workgroup waiting; a stretch may hold the end of one item, several whole
+//     ones and the beginning of another.
+//   - Little work (up to kShort tiles a stretch): every item starts a stretch
+//     of its own, so that none begins inside one and short ones need no join.
+// The grid is one round of workgroups, two a compute unit (one with 256
+// channels); with many items it is larger, so that small rows can have a
+// workgroup each.  (64 bf16 rows of 1800-32768 tokens: 183 us with 512
+// stretches, 187 with 1024, 190 with 2048, 195 with each item in 16 equal
+// parts.)
+constexpr int kGrid = 512, kGridMany = 2048;
+constexpr int kFill = 256;         // stretches wanted before they grow beyond a tile a wave
+constexpr int kShort = 16;
+constexpr int kSingle = 3 * kWaves;   // items up to this are not cut: a join costs three tiles' time
+constexpr int kLine = 8;           // tiles of a stretch that is shared by items, at least
+constexpr int kMaxParts = 128;     // stretches that one item may lie in
+constexpr int kLineRows = 1024;    // rows whose lengths a workgroup sums up itself
+constexpr int kHeaderBytes = 16384;
+static_assert(4 * kGridMany <= kHeaderBytes, "a counter per stretch");
 
 // Partial results cross the chip through device-coherent accesses (cache
 // policy sc1), so that no workgroup has to write back or invalidate a cache,
@@ -91,26 +95,31 @@ __device__ __forceinline__ f32x4 ld_device(__amdgpu_buffer_rsrc_t rsrc, uint32_t
                             __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, kDeviceAux));
 }
 
-struct AttendSplit {
-  int64_t items;
-  int parts;
-  size_t stats, total;   // workspace offsets: partial outputs at kHeaderBytes, then (max, sum)
+// A call's grid and workspace: with `line`, `groups` stretches, each of which
+// has room for the outputs [kHeads][D] and (max, sum) [kHeads] of two items it
+// holds in part; else a workgroup per item and nothing in parts.
+struct AttendPlan {
+  bool line;
+  int64_t groups;
+  size_t stats, total;   // workspace offsets: outputs from kHeaderBytes, then (max, sum)
 };
 
-AttendSplit attend_split(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_len) {
+AttendPlan attend_plan(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_len) {
   const int64_t per = q_heads / kv_heads;
-  AttendSplit s;
-  s.items = T * kv_heads * ((per + kHeads - 1) / kHeads);
+  const int64_t items = T * kv_heads * ((per + kHeads - 1) / kHeads);
   const int64_t tiles = (max_len + kTile - 1) / kTile;
-  int64_t parts = 1;
-  if (s.items <= kTickets)
-    parts = std::min<int64_t>((kTargetGroups + s.items - 1) / s.items,
-                              (tiles + kMinTiles - 1) / kMinTiles);
-  s.parts = (int)std::max<int64_t>(1, std::min<int64_t>(parts, kMaxParts));
-  const int64_t n = s.parts > 1 ? s.items * s.parts * kHeads : 0;
-  s.stats = kHeaderBytes + (size_t)n * D * 4;
-  s.total = s.stats + (size_t)n * 8;
-  return s;
+  AttendPlan p;
+  p.line = T <= kLineRows && items * tiles < ((int64_t)1 << 30);
+  p.groups = items;
+  p.stats = p.total = kHeaderBytes;
+  if (p.line) {
+    const int64_t grid = 2 * items > kGrid ? kGridMany : D == 256 ? kGrid / 2 : kGrid;
+    p.groups = std::min<int64_t>(grid, items * (tiles / kWaves + 2));
+    const size_t slots = 2 * (size_t)p.groups * kHeads;
+    p.stats = kHeaderBytes + slots * D * 4;
+    p.total = p.stats + slots * 8;
+  }
+  return p;
 }
 
 // The operands of a type: products of 16 x 32 by 32 x 16, and fp32 values as
@@ -233,10 +242,36 @@ __device__ __forceinline__ float across16(float v) {
   v = row_step<0x141, MAX>(v);   // row_half_mirror
   return row_step<0x140, MAX>(v);   // row_mirror
 }
+// Inclusive sum over the wave (rows of 16, then the rows' last lanes onward).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31
+  return v;
+}
 // x plus x of the column eight further (row_ror:8).
 __device__ __forceinline__ float fold8(float x) {
   const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x128, 0xF, 0xF, false);
   return x + __builtin_bit_cast(float, o);
+}
+
+// With 256 channels the sums of the products live in accumulation registers.
+// The compiler puts no wait states between a product and a branch whose target
+// reads them back (v_accvgpr_read), and the read then returns the old value:
+// the waits are written here, with the registers passed through, so that every
+// read comes after them.
+template <int D, int N>
+__device__ __forceinline__ void settle(f32x4 (&x)[N]) {
+  if constexpr (D == 256) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+a"(x[i]));   // every product is issued
+    asm volatile("s_nop 15\n\ts_nop 3");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+a"(x[i]));   // no read comes before
+  }
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -251,147 +286,312 @@ __device__ __forceinline__ float pow2_inverse(float p) {   // of a power of two
   return __builtin_bit_cast(float, (254u << 23) - __builtin_bit_cast(uint32_t, p));
 }
 
-template <int DT, int D>
+template <int DT, int D, bool FOLD>
 struct Shape {
   static constexpr int kBytes = Frag<DT>::kBytes;
+  static constexpr int kCols = FOLD ? 8 : kHeads;          // query heads of a product
   static constexpr int kPieces = D * kBytes / 64;          // 16-byte pieces per lane and token
   static constexpr int kRow = D * kBytes + 16;             // value row in LDS
-  static constexpr int kWaveLds = kTile * kRow > kHeads * D * 4 ? kTile * kRow : kHeads * D * 4;
+  static constexpr int kWaveLds = kTile * kRow > kCols * D * 4 ? kTile * kRow : kCols * D * 4;
 };
 
-template <int DT, int D>
+template <int DT, int D, bool FOLD, bool FEW>
 struct AttendShared {
-  __attribute__((aligned(16))) uint8_t tile[kWaves][Shape<DT, D>::kWaveLds];
+  typedef Shape<DT, D, FOLD> S;
+  __attribute__((aligned(16))) uint8_t tile[kWaves][S::kWaveLds];   // values, then outputs
   float scales[kWaves][2][kTile];      // 8-bit caches: the tile's key and value scales
   float m[kWaves][kHeads], l[kWaves][kHeads], unit[kWaves];
-  float weight[kHeads][kMaxParts];     // of the joined parts
+  float weight[S::kCols][kMaxParts];   // of the joined parts
+  int32_t start[FEW ? 1 : kLineRows + 1];   // tiles before each row
+  int32_t wave_sum[kWaves], wave_max[kWaves];
   uint32_t last;
 };
 
-template <int DT, int D, bool FOLD>
+// An item's tiles [first, end) in a stretch.
+struct Segment {
+  int t, len, table_row;   // row, its tokens, its row of the table
+  int in_row;              // which of the row's items
+  int first, end, tiles;
+  int item0, next;         // places in the line: of the item, behind the segment
+};
+
+// What the host works out once: query heads per key/value head, groups of
+// heads, items per row.
+struct AttendGrid {
+  int64_t stats_off;
+  int32_t line, per, groups, row_items, grid;
+};
+
+// FEW: up to 64 rows, whose lengths every wave holds a lane each.  (A kernel of
+// its own, because a small call's time is a chain of first fetches, of
+// instructions too: branches around the other cases' code cost it 1-2 us.)
+template <int DT, int D, bool FOLD, bool FEW>
 __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
-attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
+attend_kernel(AttendArgs a, AttendGrid g0) {
   typedef Frag<DT> F;
   typedef typename F::V V;
-  typedef Shape<DT, D> S;
+  typedef Shape<DT, D, FOLD> S;
   constexpr bool kI8 = DT == BITNET_KV_INT8;
   constexpr int kSteps = D / 32;       // contraction steps of the scores
   constexpr int kBlocks = D / 16;      // channel blocks of the outputs
   constexpr int kProducts = F::products(FOLD);
   constexpr float kUp = F::kHalf ? 14.0f : 0.0f;   // probabilities are scaled by 2^kUp
-  __shared__ AttendShared<DT, D> sh;
+  __shared__ AttendShared<DT, D, FOLD, FEW> sh;
 
   const int lane = threadIdx.x & 63, c = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool second = FOLD && c >= 8;
   const int col = FOLD ? c & 7 : c;    // this lane's head
-  const int per = a.q_heads / a.c.kv_heads;
-  const int groups = (per + kHeads - 1) / kHeads;
-  const int part = parts > 1 ? blockIdx.x : 0;
-  const int item = parts > 1 ? blockIdx.y : blockIdx.x;
-  const int t = item / (a.c.kv_heads * groups);
-  const int kvh = item / groups % a.c.kv_heads;
-  const int head0 = kvh * per + item % groups * kHeads;   // first query head
-  const int nh = min(kHeads, per - item % groups * kHeads);
+  // The arguments take several cache lines: asked for together here, not one
+  // after the other where they are used.
+  asm volatile("" ::"s"(a.q), "s"(a.tables), "s"(a.c.k), "s"(a.c.v), "s"(a.c.page_stride),
+               "s"(a.c.pages), "s"(a.out), "s"(a.ws), "s"(a.scale), "s"(a.lens), "s"(a.rows),
+               "s"(g0.grid), "s"(g0.line), "s"(a.lse));
+  const bool line = FEW || g0.line != 0;
+  const int per = g0.per, row_items = g0.row_items;
+  const int groups = FOLD ? 1 : g0.groups;
 
-  // The queries: asked for first, used once the first rows are on their way.
-  f32x4 qx[kSteps][2];
-  {
-    const float *src = a.q + t * a.q_stride + (int64_t)(head0 + min(col, nh - 1)) * D;
-#pragma unroll
-    for (int f = 0; f < kSteps; ++f) {
-      const int d = kI8 ? (f >> 1) * 64 + 16 * h + (f & 1) * 8 : f * 32 + 8 * h;
-      qx[f][0] = ld_global<f32x4>(src + d);
-      qx[f][1] = ld_global<f32x4>(src + d + 4);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  }
-
-  const int r = a.rows ? a.rows[t] : t;
-  const int len = r >= 0 && r < a.table_rows ? min(max(a.lens[t], 0), a.max_len) : 0;
-  const int tiles = (len + kTile - 1) / kTile;
-  const int share = max((tiles + parts - 1) / parts, kMinTiles);
-  const int used = max((tiles + share - 1) / share, 1);   // parts with work
-  if (part >= used) return;
-  const int first = part * share, end = min(first + share, tiles);
-
-  // Rows of the cache.
-  const int64_t head_off = (int64_t)kvh * a.c.head_stride * S::kBytes + 16 * h;
-  const uint8_t *kbase = reinterpret_cast<const uint8_t *>(a.c.k) + head_off;
-  const uint8_t *vbase = reinterpret_cast<const uint8_t *>(a.c.v) + head_off;
-  const int32_t *table = a.tables + (int64_t)max(min(r, a.table_rows - 1), 0) * a.max_pages;
-  const uint32_t page_bytes = (uint32_t)(a.c.page_stride * S::kBytes);
-  const uint32_t tok_bytes = (uint32_t)(a.c.token_stride * S::kBytes);
-  const int tok_mask = (1 << a.c.page_shift) - 1;
-
-  int pg[2];                       // pages of tokens c, c + 16 of the tile after the loaded one
-  u32x4 kr[2][S::kPieces], vr[2][S::kPieces];
-  float ksc[2], vsc[2];
-  uint32_t mask_next;              // tokens of the loaded tile that are there
-  uint64_t off[2];
-
-  auto load_pages = [&](int tile) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = min(tile * kTile + c + 16 * i, len - 1);
-      pg[i] = ld_global<int>(table + (j >> a.c.page_shift));
-    }
-    __builtin_amdgcn_sched_barrier(0);
+  auto table_row = [&](int t) { return a.rows ? a.rows[t] : t; };
+  auto length = [&](int t, int r) {
+    return r >= 0 && r < a.table_rows ? min(max(a.lens[t], 0), a.max_len) : 0;
   };
-  auto place = [&](int tile) {   // from pg: row offsets and mask of this tile
-    uint32_t m[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = tile * kTile + c + 16 * i;
-      const bool ok = tile < end && j < len && (uint32_t)pg[i] < (uint32_t)a.c.pages;
-      const uint32_t page = ok ? pg[i] : 0, tok = ok ? j & tok_mask : 0;
-      off[i] = (uint64_t)page * page_bytes + (uint64_t)tok * tok_bytes;
-      if constexpr (kI8) {
-        const uint32_t at = ((page * (uint32_t)a.c.kv_heads + kvh) << a.c.page_shift) + tok;
-        const float ks = ld_global<float>(a.c.k_scale + at), vs = ld_global<float>(a.c.v_scale + at);
-        ksc[i] = ok ? ks : 0.0f;
-        vsc[i] = ok ? vs : 0.0f;
+  auto tiles_of = [](int n) { return (n + kTile - 1) / kTile; };
+
+  // This workgroup's stretch [pos, stop) of the line.
+  int my_row = 0, my_len = 0, my_start = 0;
+  int pos = 0, stop = 1, stretch = 1;
+  bool apart = false;                  // every item starts a stretch
+  // (Exact: the quotients are below 2^13, so half a unit outweighs the error of
+  // the reciprocal.)
+  auto padded = [&](int tiles) {
+    if (!apart) return tiles;
+    return (int)(((float)(tiles + stretch - 1) + 0.5f) * __builtin_amdgcn_rcpf((float)stretch)) *
+           stretch;
+  };
+  if (line) {
+    const int each = (a.T + kThreads - 1) / kThreads;
+    const int t0 = threadIdx.x * each, t1 = min(t0 + each, a.T);
+    int raw, most;
+    if constexpr (FEW) {
+      if (lane < a.T) {
+        my_row = table_row(lane);
+        my_len = length(lane, my_row);
       }
-      m[i] = (uint32_t)__ballot(ok) & 0xffffu;
+      raw = __builtin_amdgcn_readlane(wave_scan(tiles_of(my_len)), 63);
+      most = tiles_of((int)across16<true>(across4((float)my_len)));
+    } else {
+      int sum = 0, top = 0;
+      for (int t = t0; t < t1; ++t) {
+        const int n = tiles_of(length(t, table_row(t)));
+        sum += n;
+        top = max(top, n);
+      }
+      sum = wave_scan(sum);
+      top = (int)across16<true>(across4((float)top));
+      if (lane == 63) {
+        sh.wave_sum[wave] = sum;
+        sh.wave_max[wave] = top;
+      }
+      __syncthreads();
+      raw = most = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        raw += sh.wave_sum[w];
+        most = max(most, sh.wave_max[w]);
+      }
+      __syncthreads();
     }
-    mask_next = m[0] | (m[1] << 16);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  auto load_rows = [&](const uint8_t *base, u32x4 (&x)[2][S::kPieces]) {
+    // (A length's rounding to fp32 is far below the slack of kMaxParts.)
+    raw = __builtin_amdgcn_readfirstlane(raw) * row_items;
+    most = __builtin_amdgcn_readfirstlane(most);
+    const int grid = g0.grid;
+    const int least = most / (kMaxParts - 2) + 1;
+    auto whole_rounds = [](int n) { return (n + kWaves - 1) & ~(kWaves - 1); };
+    stretch = whole_rounds(max(max((raw + kFill - 1) / kFill, most <= kSingle ? kSingle : 1), least));
+    apart = stretch <= kShort && a.T * row_items * stretch + raw <= grid * stretch;
+    if (!apart)
+      stretch = whole_rounds(max(max((int)(((uint32_t)raw + grid - 1) / (uint32_t)grid), kLine),
+                                 least));
+    int total;
+    if constexpr (FEW) {
+      const int n = padded(tiles_of(my_len)), upto = wave_scan(n);
+      my_start = upto - n;
+      total = __builtin_amdgcn_readlane(upto, 63);
+    } else {
+      int sum = 0;
+      for (int t = t0; t < t1; ++t) sum += padded(tiles_of(length(t, table_row(t))));
+      const int upto = wave_scan(sum);
+      if (lane == 63) sh.wave_sum[wave] = upto;
+      __syncthreads();
+      int before = upto - sum;
+      total = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int p = 0; p < S::kPieces; ++p) x[i][p] = ld_global<u32x4>(base + off[i] + 64 * p);
-    // Waits count loads in order of issue, so the groups stay in order.
-    __builtin_amdgcn_sched_barrier(0);
+      for (int w = 0; w < kWaves; ++w) {
+        before += w < wave ? sh.wave_sum[w] : 0;
+        total += sh.wave_sum[w];
+      }
+      for (int t = t0; t < t1; ++t) {
+        sh.start[t] = before;
+        before += padded(tiles_of(length(t, table_row(t))));
+      }
+      if (threadIdx.x == 0) sh.start[a.T] = total;
+      __syncthreads();
+    }
+    total = __builtin_amdgcn_readfirstlane(total) * row_items;
+    pos = (int)min((int64_t)blockIdx.x * stretch, (int64_t)total);
+    stop = min(pos + stretch, total);
+    // Rows without tokens lie in no stretch.
+    for (int t = blockIdx.x; t < a.T; t += grid) {
+      if (FEW ? __builtin_amdgcn_readlane(my_len, t) != 0 : sh.start[t] != sh.start[t + 1])
+        continue;
+      for (int i = threadIdx.x; i < a.q_heads * (D / 4); i += kThreads)
+        st_global<f32x4>(a.out + (int64_t)t * a.q_heads * D + 4 * i, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+      if (a.lse)
+        for (int i = threadIdx.x; i < a.q_heads; i += kThreads)
+          a.lse[(int64_t)t * a.q_heads + i] = -INFINITY;
+    }
+  }
+  const int begin = pos;
+
+  auto locate = [&]() {
+    Segment g;
+    if (!line) {   // a workgroup per item
+      g.t = blockIdx.x / row_items;
+      g.in_row = blockIdx.x - g.t * row_items;
+      g.table_row = table_row(g.t);
+      g.len = length(g.t, g.table_row);
+      g.tiles = g.end = tiles_of(g.len);
+      g.first = g.item0 = 0;
+      g.next = stop;
+      return g;
+    }
+    int row0;   // the last row that starts at or before pos
+    if constexpr (FEW) {
+      g.t = __builtin_popcountll(__ballot(lane < a.T && my_start * row_items <= pos)) - 1;
+      g.len = __builtin_amdgcn_readlane(my_len, g.t);
+      g.table_row = __builtin_amdgcn_readlane(my_row, g.t);
+      row0 = __builtin_amdgcn_readlane(my_start, g.t) * row_items;
+    } else {
+      int lo = 0, hi = a.T - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (sh.start[mid] * row_items <= pos) lo = mid; else hi = mid - 1;
+      }
+      g.t = __builtin_amdgcn_readfirstlane(lo);
+      g.table_row = table_row(g.t);
+      g.len = length(g.t, g.table_row);
+      row0 = __builtin_amdgcn_readfirstlane(sh.start[g.t]) * row_items;
+    }
+    g.tiles = tiles_of(g.len);
+    const int space = padded(g.tiles);
+    g.in_row = row_items <= 64 ? __builtin_popcountll(
+                                     __ballot(lane < row_items && lane * space <= pos - row0)) - 1
+                               : (int)((uint32_t)(pos - row0) / (uint32_t)space);
+    g.item0 = row0 + g.in_row * space;
+    g.first = pos - g.item0;
+    g.end = min(g.tiles, stop - g.item0);
+    g.next = min(g.item0 + space, stop);
+    return g;
   };
 
-  float m = -INFINITY, l = 0.0f;
-  f32x4 o[kBlocks];
-#pragma unroll
-  for (int b = 0; b < kBlocks; ++b) o[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  float vmax = pow2_above(0.0f);   // 8-bit caches: o is in units of this
+  while (pos < stop) {
+    const Segment g = locate();
+    const int kvh = FOLD ? g.in_row : g.in_row / groups;
+    const int head0 = kvh * per + (g.in_row - kvh * groups) * kHeads;   // first query head
+    const int nh = min(kHeads, per - (g.in_row - kvh * groups) * kHeads);
+    const bool whole = g.first == 0 && g.end == g.tiles;
 
-  int tile = first + wave;
-  if (tile < end) {
-    load_pages(tile);
-    place(tile);
-    load_pages(tile + kWaves);
-    load_rows(vbase, vr);
-    load_rows(kbase, kr);
+    // Rows of the cache.
+    const int64_t head_off = (int64_t)kvh * a.c.head_stride * S::kBytes + 16 * h;
+    const uint8_t *kbase = reinterpret_cast<const uint8_t *>(a.c.k) + head_off;
+    const uint8_t *vbase = reinterpret_cast<const uint8_t *>(a.c.v) + head_off;
+    const int32_t *table = a.tables + (int64_t)max(min(g.table_row, a.table_rows - 1), 0) * a.max_pages;
+    const uint32_t page_bytes = (uint32_t)(a.c.page_stride * S::kBytes);
+    const uint32_t tok_bytes = (uint32_t)(a.c.token_stride * S::kBytes);
+    const int tok_mask = (1 << a.c.page_shift) - 1;
+
+    int pg[2];                       // pages of tokens c, c + 16 of the tile after the loaded one
+    u32x4 kr[2][S::kPieces], vr[2][S::kPieces];
+    float ksc[2], vsc[2];
+    uint32_t mask_next;              // tokens of the loaded tile that are there
+    uint64_t off[2];
+
+    auto load_pages = [&](int tile) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = min(tile * kTile + c + 16 * i, g.len - 1);
+        pg[i] = ld_global<int>(table + (j >> a.c.page_shift));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto place = [&](int tile) {   // from pg: row offsets and mask of this tile
+      uint32_t m[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = tile * kTile + c + 16 * i;
+        const bool ok = j < g.len && (uint32_t)pg[i] < (uint32_t)a.c.pages;
+        const uint32_t page = ok ? pg[i] : 0, tok = ok ? j & tok_mask : 0;
+        off[i] = (uint64_t)page * page_bytes + (uint64_t)tok * tok_bytes;
+        if constexpr (kI8) {
+          const uint32_t at = ((page * (uint32_t)a.c.kv_heads + kvh) << a.c.page_shift) + tok;
+          const float ks = ld_global<float>(a.c.k_scale + at);
+          const float vs = ld_global<float>(a.c.v_scale + at);
+          ksc[i] = ok ? ks : 0.0f;
+          vsc[i] = ok ? vs : 0.0f;
+        }
+        m[i] = (uint32_t)__ballot(ok) & 0xffffu;
+      }
+      mask_next = m[0] | (m[1] << 16);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto load_rows = [&](const uint8_t *base, u32x4 (&x)[2][S::kPieces]) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int p = 0; p < S::kPieces; ++p) x[i][p] = ld_global<u32x4>(base + off[i] + 64 * p);
+      // Waits count loads in order of issue, so the groups stay in order.
+      __builtin_amdgcn_sched_barrier(0);
+    };
+
+    int tile = g.first + wave;
+    if (tile < g.end) load_pages(tile);
+    // The queries: asked for early, used once the first rows are on their way.
+    f32x4 qx[kSteps][2];
+    {
+      const float *src = a.q + g.t * a.q_stride + (int64_t)(head0 + min(col, nh - 1)) * D;
+#pragma unroll
+      for (int f = 0; f < kSteps; ++f) {
+        const int d = kI8 ? (f >> 1) * 64 + 16 * h + (f & 1) * 8 : f * 32 + 8 * h;
+        qx[f][0] = ld_global<f32x4>(src + d);
+        qx[f][1] = ld_global<f32x4>(src + d + 4);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (tile < g.end) {
+      place(tile);
+      load_rows(kbase, kr);
+      load_rows(vbase, vr);
+      load_pages(tile + kWaves);
+    }
+
+    // The stretches that hold the item: `used` of them from w0 on.
+    int w0 = 0, used = 1;
+    if (!whole) {
+      w0 = (uint32_t)g.item0 / (uint32_t)stretch;
+      used = (uint32_t)(g.item0 + g.tiles - 1) / (uint32_t)stretch - w0 + 1;
+    }
 
     // Queries as terms.
     V q[kSteps][kProducts];
-    float unscale = 1.0f;
+    float unscale = 1.0f;   // of the scores
     {
-      float x[kSteps][8];
       float big = 0.0f;
 #pragma unroll
       for (int f = 0; f < kSteps; ++f)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[f][e] = qx[f][e >> 2][e & 3] * (a.scale * kLog2e);
-          big = fmaxf(big, fabsf(x[f][e]));
+          qx[f][e >> 2][e & 3] *= a.scale * kLog2e;
+          big = fmaxf(big, fabsf(qx[f][e >> 2][e & 3]));
         }
       float up = 1.0f;
       if constexpr (F::kHalf) {
@@ -401,34 +601,36 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
       }
 #pragma unroll
       for (int f = 0; f < kSteps; ++f) {
+        float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[f][e] *= up;
-        F::template split<FOLD>(x[f], second, q[f]);
+        for (int e = 0; e < 8; ++e) x[e] = qx[f][e >> 2][e & 3] * up;
+        F::template split<FOLD>(x, second, q[f]);
       }
     }
 
+    float m = -INFINITY, l = 0.0f;   // m in units of 1 / unscale
+    f32x4 o[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) o[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    float vmax = pow2_above(0.0f);   // 8-bit caches: o is in units of this
     uint8_t *rows = sh.tile[wave];
-    for (; tile < end; tile += kWaves) {
+
+    for (; tile < g.end; tile += kWaves) {
       const uint32_t mask = mask_next;
       const bool all = mask == 0xffffffffu;
-      // Values into LDS, as rows; scales too.
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bool here = all || ((mask >> (c + 16 * i)) & 1);
-#pragma unroll
-        for (int pc = 0; pc < S::kPieces; ++pc) {
-          u32x4 v = vr[i][pc];
-          if (!here) v = u32x4{0u, 0u, 0u, 0u};
-          *reinterpret_cast<u32x4 *>(rows + (c + 16 * i) * S::kRow + 64 * pc + 16 * h) = v;
-        }
-      }
-      float ks[8], vs[8];
+      // Scales, from a lane per token to the scores' layout; the values' relative
+      // to the power of two above the largest so far.
+      float ks[8], vs[8], vkeep = 1.0f;
       if constexpr (kI8) {
+        const float v_new = fmaxf(vmax, pow2_above(across16<true>(fmaxf(vsc[0], vsc[1]))));
+        const float inv = pow2_inverse(v_new);
+        vkeep = vmax * inv;
+        vmax = v_new;
         if (h == 0) {
           sh.scales[wave][0][c] = ksc[0];
           sh.scales[wave][0][c + 16] = ksc[1];
-          sh.scales[wave][1][c] = vsc[0];
-          sh.scales[wave][1][c + 16] = vsc[1];
+          sh.scales[wave][1][c] = vsc[0] * inv;
+          sh.scales[wave][1][c + 16] = vsc[1] * inv;
         }
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -437,47 +639,59 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
           const f32x4 vs4 = *reinterpret_cast<const f32x4 *>(&sh.scales[wave][1][16 * i + 4 * h]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            ks[4 * i + e] = ks4[e] * unscale;
+            ks[4 * i + e] = ks4[e];
             vs[4 * i + e] = vs4[e];
           }
         }
       }
-      // The next tile's values.
-      place(tile + kWaves);
-      load_pages(tile + 2 * kWaves);
-      load_rows(vbase, vr);
-
       // Scores of tokens 16 i + 4 h + e for this column.
-      f32x4 s[2][2];
+      f32x4 s[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+      for (int f = 0; f < kSteps; ++f) {
+        V k[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (kI8)
+            k[i] = f & 1 ? codes_f16(kr[i][f >> 1].z, kr[i][f >> 1].w)
+                         : codes_f16(kr[i][f >> 1].x, kr[i][f >> 1].y);
+          else
+            k[i] = __builtin_bit_cast(V, kr[i][f]);
+        }
+#pragma unroll
+        for (int p = kProducts - 1; p >= 0; --p)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) s[i] = F::mfma(k[i], q[f][p], s[i]);
+      }
+      settle<D>(s);
+      // Values into LDS, as rows.
+      if (!all)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (!((mask >> (c + 16 * i)) & 1))
+#pragma unroll
+            for (int pc = 0; pc < S::kPieces; ++pc) vr[i][pc] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) s[i][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int f = 0; f < kSteps; ++f)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          V k;
-          if constexpr (kI8)
-            k = f & 1 ? codes_f16(kr[i][f >> 1].z, kr[i][f >> 1].w)
-                      : codes_f16(kr[i][f >> 1].x, kr[i][f >> 1].y);
-          else
-            k = __builtin_bit_cast(V, kr[i][f]);
-#pragma unroll
-          for (int p = kProducts - 1; p >= 0; --p) s[i][f & 1] = F::mfma(k, q[f][p], s[i][f & 1]);
-        }
-      // The next tile's keys.
+        for (int pc = 0; pc < S::kPieces; ++pc)
+          *reinterpret_cast<u32x4 *>(rows + (c + 16 * i) * S::kRow + 64 * pc + 16 * h) = vr[i][pc];
+      // The next tile.
       __builtin_amdgcn_sched_barrier(0);
-      load_rows(kbase, kr);
+      if (tile + kWaves < g.end) {
+        place(tile + kWaves);
+        load_rows(kbase, kr);
+        load_rows(vbase, vr);
+        load_pages(tile + 2 * kWaves);
+      }
 
       float x[8];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float y = s[i][0][e] + s[i][1][e];
+          float y = s[i][e];
           if constexpr (FOLD) y = fold8(y);
-          y *= kI8 ? ks[4 * i + e] : unscale;
+          if constexpr (kI8) y *= ks[4 * i + e];
           x[4 * i + e] = y;
         }
       if (!all)
@@ -491,29 +705,19 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
       for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
       const float m_new = fmaxf(m, across4(top));
       const float base = m_new == -INFINITY ? 0.0f : m_new;
-      const float lkeep = exp2_fast(m - base);
-      float keep = lkeep;
-      float inv = 1.0f;
-      if constexpr (kI8) {
-        float vt = vs[0];
-#pragma unroll
-        for (int e = 1; e < 8; ++e) vt = fmaxf(vt, vs[e]);
-        const float v_new = fmaxf(vmax, pow2_above(across4(vt)));
-        inv = pow2_inverse(v_new);
-        keep *= vmax * inv;
-        vmax = v_new;
-      }
+      const float lkeep = exp2_fast((m - base) * unscale);
+      const float keep = lkeep * vkeep;
       m = m_new;
       float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] = exp2_fast(x[e] - (base - kUp));
+        x[e] = exp2_fast(__builtin_fmaf(x[e] - base, unscale, kUp));
         sum += x[e];
       }
       l = l * lkeep + sum;   // not in units of vmax
       if constexpr (kI8)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= vs[e] * inv;
+        for (int e = 0; e < 8; ++e) x[e] *= vs[e];
       if (__any(keep != 1.0f))
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) o[b] *= keep;
@@ -541,146 +745,188 @@ attend_kernel(AttendArgs a, int parts, int64_t stats_off) {
 #pragma unroll
         for (int i = kProducts - 1; i >= 0; --i) o[b] = F::mfma(v, p[i], o[b]);
       }
+      settle<D>(o);
       __builtin_amdgcn_wave_barrier();
     }
+    m *= unscale;
     if constexpr (FOLD)
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[b][e] = fold8(o[b][e]);
-  }
 
-  // Join the waves: outputs 16 b + 4 h + e of head c, each wave's relative to
-  // its own maximum (folded: columns 8-15 repeat heads 0-7 and are left out).
-  l = sum4(l);
-  if (h == 0) {
-    sh.m[wave][c] = m;
-    sh.l[wave][c] = l;
-  }
-  if (lane == 0) sh.unit[wave] = vmax;
-  f32x4 *mine = reinterpret_cast<f32x4 *>(sh.tile[wave]);
-#pragma unroll
-  for (int b = 0; b < kBlocks; ++b)
-    if (!second) mine[c * (D / 4) + 4 * b + h] = o[b];
-  __syncthreads();
-  constexpr int kQuads = D / 4;        // of a head
-  const int n4 = nh * kQuads;
-  // Workspace of this item: outputs [parts][kHeads][D], (max, sum) [parts][kHeads].
-  const uint32_t part_bytes = kHeads * D * 4;
-  const __amdgpu_buffer_rsrc_t outs =
-      make_rsrc(a.ws + kHeaderBytes + (int64_t)item * parts * part_bytes, parts * part_bytes);
-  f32x2 *stats = reinterpret_cast<f32x2 *>(a.ws + stats_off) + (int64_t)item * parts * kHeads;
-  f32x4 *out = reinterpret_cast<f32x4 *>(a.out + ((int64_t)t * a.q_heads + head0) * D);
-  auto finish = [&](int i, int head, f32x4 sum, float tm, float tl) {
-    st_global<f32x4>(out + i, tl > 0.0f ? sum / tl : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-    if (a.lse && i % kQuads == 0)
-      a.lse[(int64_t)t * a.q_heads + head0 + head] =
-          tl > 0.0f ? (tm - kUp + __log2f(tl)) * kLn2 : -INFINITY;
-  };
-  for (int i = threadIdx.x; i < n4; i += kThreads) {
-    const int head = i / kQuads;
-    float tm = sh.m[0][head];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) tm = fmaxf(tm, sh.m[w][head]);
-    const float base = tm == -INFINITY ? 0.0f : tm;
-    float tl = 0.0f;
-    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = exp2_fast(sh.m[w][head] - base);
-      tl += sh.l[w][head] * f;
-      sum += reinterpret_cast<const f32x4 *>(sh.tile[w])[i] * (kI8 ? f * sh.unit[w] : f);
+    // Join the waves: outputs 16 b + 4 h + e of head c, each wave's relative to
+    // its own maximum (folded: columns 8-15 repeat heads 0-7 and are left out).
+    l = sum4(l);
+    if (h == 0) {
+      sh.m[wave][c] = m;
+      sh.l[wave][c] = l;
     }
-    if (used == 1) {
-      finish(i, head, sum, tm, tl);
-    } else {
-      st_device(outs, part * part_bytes + 16 * i, sum);
-      if (i % kQuads == 0)
-        __hip_atomic_store((BITNET_GLOBAL uint64_t *)&stats[part * kHeads + head],
-                           __builtin_bit_cast(uint64_t, f32x2{tm, tl}), __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
+    if (lane == 0) sh.unit[wave] = vmax;
+    constexpr int kQuads = D / 4;        // of a head
+    f32x4 *mine = reinterpret_cast<f32x4 *>(sh.tile[wave]);
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+      if (!second) mine[c * kQuads + 4 * b + h] = o[b];
+    __syncthreads();
+    const int n4 = nh * kQuads;
+    // This stretch's two places in the workspace: for the item at its beginning
+    // and for one that begins inside it and goes on behind it.
+    constexpr uint32_t kPartBytes = kHeads * D * 4;
+    const int my_place = 2 * blockIdx.x + (pos == begin ? 0 : 1);
+    const __amdgpu_buffer_rsrc_t outs =
+        make_rsrc(a.ws + kHeaderBytes, line ? 2 * g0.grid * kPartBytes : 0);
+    f32x2 *stats = reinterpret_cast<f32x2 *>(a.ws + g0.stats_off);
+    f32x4 *out = reinterpret_cast<f32x4 *>(a.out + ((int64_t)g.t * a.q_heads + head0) * D);
+    auto finish = [&](int i, int head, f32x4 sum, float tm, float tl) {
+      st_global<f32x4>(out + i, tl > 0.0f ? sum / tl : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+      if (a.lse && i % kQuads == 0)
+        a.lse[(int64_t)g.t * a.q_heads + head0 + head] =
+            tl > 0.0f ? (tm - kUp + __log2f(tl)) * kLn2 : -INFINITY;
+    };
+    for (int i = threadIdx.x; i < n4; i += kThreads) {
+      const int head = i / kQuads;
+      float tm = sh.m[0][head];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) tm = fmaxf(tm, sh.m[w][head]);
+      const float base = tm == -INFINITY ? 0.0f : tm;
+      float tl = 0.0f;
+      f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = exp2_fast(sh.m[w][head] - base);
+        tl += sh.l[w][head] * f;
+        sum += reinterpret_cast<const f32x4 *>(sh.tile[w])[i] * (kI8 ? f * sh.unit[w] : f);
+      }
+      if (whole) {
+        finish(i, head, sum, tm, tl);
+      } else {
+        st_device(outs, my_place * kPartBytes + 16 * i, sum);
+        if (i % kQuads == 0)
+          __hip_atomic_store((BITNET_GLOBAL uint64_t *)&stats[my_place * kHeads + head],
+                             __builtin_bit_cast(uint64_t, f32x2{tm, tl}), __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+      }
     }
-  }
-  if (used == 1) return;
 
-  // The last part to arrive joins them all; it leaves the counter at zero.
-  // Each wave's stores have been acknowledged before the counter moves.
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    uint32_t *ticket = reinterpret_cast<uint32_t *>(a.ws) + item;
-    const uint32_t n =
-        __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    sh.last = n == (uint32_t)used - 1;
-    if (sh.last) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  if (!sh.last) return;
-  // Wave w adds up parts w, w + kWaves, ..., a lane per four channels in each
-  // of kWide stretches of the outputs; the loads of kJoin parts go out at once,
-  // the first ones before the weights are known.
-  constexpr int kWide = (FOLD ? 8 : kHeads) * kQuads / 64;
-  constexpr int kJoin = kWide >= 8 ? 2 : 16 / kWide;
-  f32x4 x[kJoin][kWide], sum[kWide];
-  auto load_parts = [&](int p0) {
+    if (!whole) {
+      // The last stretch of the item to arrive joins its parts; it leaves the
+      // counter, the first stretch's, at zero.  Each wave's stores have been
+      // acknowledged before the counter moves.
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        uint32_t *ticket = reinterpret_cast<uint32_t *>(a.ws) + w0;
+        const uint32_t n =
+            __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        sh.last = n == (uint32_t)used - 1;
+        if (sh.last) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __syncthreads();
+      if (sh.last) {
+        // Part p is at the beginning of stretch w0 + p, unless the item begins
+        // inside its first stretch.
+        const int inside = g.item0 != w0 * stretch ? 1 : 0;
+        auto place_of = [&](int p) { return 2 * (w0 + p) + (p == 0 ? inside : 0); };
+        // Wave w adds up parts w, w + kWaves, ..., a lane per four channels in
+        // each of kWide blocks of the outputs; the loads of kJoin parts go out at
+        // once, the first ones before the weights are known.
+        constexpr int kWide = S::kCols * kQuads / 64;
+        constexpr int kJoin = kWide >= 8 ? 2 : 16 / kWide;
+        f32x4 x[kJoin][kWide], sum[kWide];
+        auto load_parts = [&](int p0) {
 #pragma unroll
-    for (int u = 0; u < kJoin; ++u)
+          for (int u = 0; u < kJoin; ++u)
 #pragma unroll
-      for (int b = 0; b < kWide; ++b)
-        x[u][b] = ld_device(outs, min(p0 + u * kWaves, used - 1) * part_bytes +
-                                      16 * min(64 * b + lane, n4 - 1));
-  };
-  load_parts(wave);
-  // A wave per head turns the parts' maxima and sums into weights.
-  for (int head = wave; head < nh; head += kWaves) {
-    f32x2 st = {-INFINITY, 0.0f};
-    if (lane < used)
-      st = __builtin_bit_cast(f32x2, (uint64_t)__hip_atomic_load(
-                                         (const BITNET_GLOBAL uint64_t *)&stats[lane * kHeads + head],
-                                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-    const float tm = across16<true>(across4(st.x));
-    const float f = exp2_fast(st.x - (tm == -INFINITY ? 0.0f : tm));
-    const float tl = across16<false>(sum4(st.y * f));
-    if (lane < used) sh.weight[head][lane] = f;
-    if (lane == 0) {
-      sh.m[0][head] = tm;
-      sh.l[0][head] = tl;
-    }
-  }
-  __syncthreads();
+            for (int b = 0; b < kWide; ++b)
+              x[u][b] = ld_device(outs, place_of(min(p0 + u * kWaves, used - 1)) * kPartBytes +
+                                            16 * min(64 * b + lane, n4 - 1));
+        };
+        load_parts(wave);
+        // A wave per head turns the parts' maxima and sums into weights.
+        for (int head = wave; head < nh; head += kWaves) {
+          f32x2 st[kMaxParts / 64];
+          float tm = -INFINITY;
 #pragma unroll
-  for (int b = 0; b < kWide; ++b) sum[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int p0 = wave; p0 < used; p0 += kJoin * kWaves) {
-    if (p0 != wave) load_parts(p0);
+          for (int k = 0; k < kMaxParts / 64; ++k) {
+            const int p = lane + 64 * k;
+            st[k] = f32x2{-INFINITY, 0.0f};
+            if (p < used)
+              st[k] = __builtin_bit_cast(
+                  f32x2, (uint64_t)__hip_atomic_load(
+                             (const BITNET_GLOBAL uint64_t *)&stats[place_of(p) * kHeads + head],
+                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+            tm = fmaxf(tm, st[k].x);
+          }
+          tm = across16<true>(across4(tm));
+          float tl = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kJoin; ++u)
-      if (p0 + u * kWaves < used)
+          for (int k = 0; k < kMaxParts / 64; ++k) {
+            const int p = lane + 64 * k;
+            const float f = exp2_fast(st[k].x - (tm == -INFINITY ? 0.0f : tm));
+            tl += st[k].y * f;
+            if (p < used) sh.weight[head][p] = f;
+          }
+          tl = across16<false>(sum4(tl));
+          if (lane == 0) {
+            sh.m[0][head] = tm;
+            sh.l[0][head] = tl;
+          }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < kWide; ++b) sum[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int p0 = wave; p0 < used; p0 += kJoin * kWaves) {
+          if (p0 != wave) load_parts(p0);
+#pragma unroll
+          for (int u = 0; u < kJoin; ++u)
+            if (p0 + u * kWaves < used)
+#pragma unroll
+              for (int b = 0; b < kWide; ++b)
+                sum[b] += x[u][b] *
+                          sh.weight[min(64 * b + lane, n4 - 1) / kQuads][p0 + u * kWaves];
+        }
 #pragma unroll
         for (int b = 0; b < kWide; ++b)
-          sum[b] += x[u][b] * sh.weight[min(64 * b + lane, n4 - 1) / kQuads][p0 + u * kWaves];
-  }
+          if (64 * b + lane < n4) mine[64 * b + lane] = sum[b];
+        __syncthreads();
+        for (int i = threadIdx.x; i < n4; i += kThreads) {
+          f32x4 all = reinterpret_cast<const f32x4 *>(sh.tile[0])[i];
 #pragma unroll
-  for (int b = 0; b < kWide; ++b)
-    if (64 * b + lane < n4) mine[64 * b + lane] = sum[b];
-  __syncthreads();
-  for (int i = threadIdx.x; i < n4; i += kThreads) {
-    f32x4 sum = reinterpret_cast<const f32x4 *>(sh.tile[0])[i];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) sum += reinterpret_cast<const f32x4 *>(sh.tile[w])[i];
-    finish(i, i / kQuads, sum, sh.m[0][i / kQuads], sh.l[0][i / kQuads]);
+          for (int w = 1; w < kWaves; ++w) all += reinterpret_cast<const f32x4 *>(sh.tile[w])[i];
+          finish(i, i / kQuads, all, sh.m[0][i / kQuads], sh.l[0][i / kQuads]);
+        }
+      }
+    }
+    pos = g.next;
+    if (pos < stop) __syncthreads();   // the next segment writes where this one reads
   }
+}
+
+template <int DT, int D, bool FOLD>
+void attend_rows(const AttendArgs &a, const AttendGrid &g, hipStream_t stream) {
+  if (a.T <= 64 && g.line)
+    attend_kernel<DT, D, FOLD, true><<<g.grid, kThreads, 0, stream>>>(a, g);
+  else
+    attend_kernel<DT, D, FOLD, false><<<g.grid, kThreads, 0, stream>>>(a, g);
 }
 
 template <int DT, bool FOLD>
 void attend_dim(const AttendArgs &a, int D, hipStream_t stream) {
-  const AttendSplit s = attend_split(a.T, a.q_heads, a.c.kv_heads, D, a.max_len);
-  const dim3 grid = s.parts > 1 ? dim3(s.parts, s.items) : dim3(s.items);
+  const AttendPlan p = attend_plan(a.T, a.q_heads, a.c.kv_heads, D, a.max_len);
+  AttendGrid g;
+  g.stats_off = (int64_t)p.stats;
+  g.line = p.line;
+  g.per = a.q_heads / a.c.kv_heads;
+  g.groups = (g.per + kHeads - 1) / kHeads;
+  g.row_items = a.c.kv_heads * g.groups;
+  g.grid = (int32_t)p.groups;
   if (D == 64)
-    attend_kernel<DT, 64, FOLD><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
+    attend_rows<DT, 64, FOLD>(a, g, stream);
   else if (D == 128)
-    attend_kernel<DT, 128, FOLD><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
+    attend_rows<DT, 128, FOLD>(a, g, stream);
   else
-    attend_kernel<DT, 256, FOLD><<<grid, kThreads, 0, stream>>>(a, s.parts, s.stats);
+    attend_rows<DT, 256, FOLD>(a, g, stream);
 }
 
 template <int DT>
@@ -695,7 +941,7 @@ void attend_type(const AttendArgs &a, int D, hipStream_t stream) {
 
 size_t attend_workspace_bytes(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                               int64_t max_len) {
-  return attend_split(T, q_heads, kv_heads, head_dim, max_len).total;
+  return attend_plan(T, q_heads, kv_heads, head_dim, max_len).total;
 }
 
 hipError_t launch_attend(const AttendArgs &a, int dtype, int head_dim, hipStream_t stream) {
