@@ -561,6 +561,20 @@ def test_select_ties_and_special_values(tb):
         check_select(tb, x, s, 2, exact_ties=True)
 
 
+@pytest.mark.parametrize("W,V", [(32, 40), (32, 20000), (4, 151936), (8, 151936), (5, 151936)])
+def test_select_everything_ties(tb, W, V):
+    """All candidates of a group equal, alive or dead; and rising logits, where
+    every tile of a row replaces what the ones before it gave."""
+    say(f"[select] ties W={W} V={V}")
+    x = np.zeros((W, V), np.float32)
+    check_select(tb, x, np.full(W, -1, np.float32), W, exact_ties=True)
+    check_select(tb, x, np.full(W, -np.inf, np.float32), W, exact_ties=True)
+    check_select(tb, x, np.full(W, -1, np.float32), W, (np.arange(W) % 2).astype(np.int32), V - 1,
+                 exact_ties=True)
+    x[:] = (np.arange(V) * 1e-3).astype(np.float32)
+    check_select(tb, x, -np.arange(W, dtype=np.float32) * 0.25, W, exact_ties=True)
+
+
 def test_select_in_place(tb):
     import torch
     say("[select] scores and flags in place, one workspace for many shapes")
