@@ -206,42 +206,6 @@ __device__ __forceinline__ f16x8 codes_f16(uint32_t lo, uint32_t hi) {
   return r;
 }
 
-// The lanes of one column are 16 apart.  The exchanges put rows 0, 2 (halves
-// 0) beside rows 1, 3 (halves 1), without leaving the registers.
-__device__ __forceinline__ float across4(float v) {   // maximum
-  const uint32_t a = __builtin_bit_cast(uint32_t, v);
-  const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-  const uint32_t p0 = p[0], p1 = p[1];   // (a bit cast of an element itself reads element 0)
-  const float m = fmaxf(__builtin_bit_cast(float, p0), __builtin_bit_cast(float, p1));
-  const uint32_t b = __builtin_bit_cast(uint32_t, m);
-  const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  const uint32_t q0 = q[0], q1 = q[1];
-  return fmaxf(__builtin_bit_cast(float, q0), __builtin_bit_cast(float, q1));
-}
-__device__ __forceinline__ float sum4(float v) {
-  const uint32_t a = __builtin_bit_cast(uint32_t, v);
-  const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-  const uint32_t p0 = p[0], p1 = p[1];
-  const float m = __builtin_bit_cast(float, p0) + __builtin_bit_cast(float, p1);
-  const uint32_t b = __builtin_bit_cast(uint32_t, m);
-  const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  const uint32_t q0 = q[0], q1 = q[1];
-  return __builtin_bit_cast(float, q0) + __builtin_bit_cast(float, q1);
-}
-// Maximum or sum over the 16 lanes of a row: quads, then mirrored halves.
-template <int CTRL, bool MAX>
-__device__ __forceinline__ float row_step(float v) {
-  const float o = __builtin_bit_cast(
-      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
-  return MAX ? fmaxf(v, o) : v + o;
-}
-template <bool MAX>
-__device__ __forceinline__ float across16(float v) {
-  v = row_step<0xB1, MAX>(v);    // quad_perm 1,0,3,2
-  v = row_step<0x4E, MAX>(v);    // quad_perm 2,3,0,1
-  v = row_step<0x141, MAX>(v);   // row_half_mirror
-  return row_step<0x140, MAX>(v);   // row_mirror
-}
 // Inclusive sum over the wave (rows of 16, then the rows' last lanes onward).
 __device__ __forceinline__ int wave_scan(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1

@@ -4,7 +4,9 @@
 // contributes at most its W largest logits (ties: the lower token), and the
 // log-softmax needs only its sum of exp.  One pass over the logits gives both;
 // they are read once and nothing else is large, so the kernel is a stream with
-// as little as possible beside it.
+// as little as possible beside it.  (The loads are non-temporal: without any
+// selection or join the stream of 256 rows of 151,936 logits runs at 6.5 TB/s
+// with them and at 5.8 without.)
 //
 // A workgroup takes one chunk of a row, 4096 logits at a time in registers.
 // Each thread keeps its own running maximum and sum of exp.  A 64-bit key (the
@@ -29,6 +31,7 @@ namespace bitnet {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kWaves = kThreads / 64;
 constexpr int kQuads = 4;                            // 16-byte loads per thread and tile
 constexpr int kPer = 4 * kQuads;                     // logits per thread and tile
@@ -40,7 +43,7 @@ constexpr int kHeaderBytes = 2 * 4 * kMaxRows;
 // Workgroups wanted before a workgroup takes more than one tile: two rounds of
 // eight a compute unit (256 rows of 151,936 logits: see below).
 #ifndef BITNET_SELECT_GROUPS
-#define BITNET_SELECT_GROUPS 2048
+#define BITNET_SELECT_GROUPS 1024
 #endif
 constexpr int kTargetGroups = BITNET_SELECT_GROUPS;
 
@@ -50,9 +53,10 @@ typedef float f32x4_row __attribute__((ext_vector_type(4), aligned(4)));
 typedef unsigned long long u64;
 
 // Chunks of a row, each of `tiles` tiles; whether a group's chunks are joined at
-// once (up to kFlat candidates) or by rows first; and the workspace: counters, then per
+// once or by rows first; and the workspace: counters, then per
 // row and chunk (max, sum) and W keys, then per row W scores and W keys.
-constexpr int kFlat = 1024;
+constexpr int kNarrow = 8;            // widths of the smaller kernel
+constexpr int kFlat = 640;            // candidates of a group that are joined at once
 struct SelectPlan {
   int chunks, tiles, flat;
   size_t stats, keys, scores, row_keys, total;
@@ -74,17 +78,25 @@ SelectPlan select_plan(int64_t rows, int64_t W, int64_t V) {
   return p;
 }
 
-__device__ __forceinline__ float clean(float x) {   // NaN and +inf count as -inf, -0 as 0
-  return x < INFINITY ? x + 0.0f : -INFINITY;
+__device__ __forceinline__ float clean(float x) {   // NaN and +inf count as -inf
+  return x < INFINITY ? x : -INFINITY;
 }
 __device__ __forceinline__ u64 key_of(float x, uint32_t token) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, x);
+  const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);   // -0 as 0
   const uint32_t o = b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
   return ((u64)o << 32) | (0xffffffffu - token);
 }
 __device__ __forceinline__ float logit_of(u64 key) {
   const uint32_t o = (uint32_t)(key >> 32);
   return __builtin_bit_cast(float, o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
+}
+// exp2 of the difference of two maxima's exponents, m <= n, n > -inf.
+__device__ __forceinline__ bool huge(float m) { return fabsf(m) > 0x1p126f; }
+__device__ __forceinline__ float shift(float m, float n) {
+  return __builtin_amdgcn_exp2f(huge(n) ? (m - n) * kLog2e : m * kLog2e - n * kLog2e);
+}
+__device__ __forceinline__ double exponent(float m) {
+  return huge(m) ? (double)m * (double)kLog2e : (double)(m * kLog2e);
 }
 // The bits of a score in unsigned order; above 0 (a score is never NaN).
 __device__ __forceinline__ u64 order_of(double t) {
@@ -101,19 +113,31 @@ __device__ __forceinline__ u64 ld_device(const void *p) {
                            __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Room for the keys that reach a bound (kMaxWidth lanes of a wave, and those that
-// were there), and for a group's candidates, which may all tie.
-constexpr int kCandidates = 3 * kFlat;
-static_assert(kCandidates >= kWaves * kMaxWidth * kPer + kMaxWidth, "keys above a bound");
-static_assert(kFlat >= kMaxWidth * kMaxWidth, "a list per row");
+// A candidate of a group: its score and its key (which holds its token).
+struct Entry {
+  double score;
+  u64 key;
+};
 
+// By the greatest width a kernel serves: room for the keys that reach a bound (as
+// many lanes of a wave, kPer keys each, and those that were there), and for a
+// group's candidates, which may all tie.
+template <int MAXW>
 struct SelectShared {
-  u64 cand[kCandidates];
-  u64 best[kMaxWidth];                 // the W largest keys, in order
+  static constexpr int kEntries = MAXW == kMaxWidth ? kMaxWidth * kMaxWidth : kFlat;
+  static constexpr int kKeys = kWaves * MAXW * kPer + MAXW;
+  static constexpr int kWords = 2 * kEntries > kKeys ? 2 * kEntries : kKeys;
+  __attribute__((aligned(16))) u64 cand[kWords];
+  u64 best[MAXW];                      // the W largest keys, in order
+  double lse[MAXW];
+  float from[MAXW];                    // scores of the group's beams, and their flags
+  int flag[MAXW];
   u64 bound[2][kWaves];
   int above[2][kWaves];
   float m[kWaves], s[kWaves];
   uint32_t count, last;
+  int winner[MAXW];
+  uint8_t beam[kEntries];              // of the entries
 };
 
 // A bound that W lanes' keys reach, and no more than W unless keys are equal
@@ -150,18 +174,24 @@ __device__ __forceinline__ u64 wave_bound(u64 key, int W) {
 }
 
 // sh.best becomes the W largest of sh.best (`have` keys, 0 or W) and of the
-// threads' keys: key(j), j < N <= kPer, 0 for none; `mine` is the thread's
-// largest.  Every thread calls it, with the workgroup in step; `flip` alternates
-// from call to call.
-template <int N, typename Key>
-__device__ __forceinline__ void select_largest(SelectShared &sh, int W, int have, int flip, u64 mine,
-                                               Key key) {
+// threads' keys: key(j), j < N <= kPer, 0 for none; mine() is the thread's
+// largest, looked at only where some lane of the wave is `hopeful`: false where
+// the thread holds nothing above sh.best[W - 1].  Every thread calls it, with
+// the workgroup in step; `flip` alternates from call to call.
+template <int N, int MAXW, typename Mine, typename Key>
+__device__ __forceinline__ void select_largest(SelectShared<MAXW> &sh, int W, int have, int flip,
+                                               bool hopeful, Mine mine_of, Key key) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const u64 floor = have ? sh.best[W - 1] : 0;
-  // A wave with few keys above what is there already needs no further bound:
-  // kMaxWidth lanes of a wave fit the list.
-  const int above = __builtin_popcountll(__ballot(mine > floor));
-  const u64 b = above > (have ? kMaxWidth : W) ? wave_bound(mine, W) : 0;
+  u64 mine = 0, b = 0;
+  int above = 0;
+  if (__any(hopeful)) {
+    mine = mine_of();
+    above = __builtin_popcountll(__ballot(mine > floor));
+    // A wave with few keys above what is there already needs no further bound:
+    // MAXW lanes of a wave fit the list.
+    if (above > (have ? MAXW : W)) b = wave_bound(mine, W);
+  }
   if (lane == 0) {
     sh.bound[flip][wave] = b;
     sh.above[flip][wave] = above;
@@ -188,6 +218,7 @@ __device__ __forceinline__ void select_largest(SelectShared &sh, int W, int have
   for (int i = tid; i < all; i += kThreads) {
     const u64 k = sh.cand[i];
     int r = 0;
+#pragma unroll 4
     for (int c = 0; c < all; ++c) r += sh.cand[c] > k ? 1 : 0;
     if (r < W) sh.best[r] = k;
   }
@@ -197,7 +228,8 @@ __device__ __forceinline__ void select_largest(SelectShared &sh, int W, int have
 
 // Counts one more arrival; true for the last of n, which leaves zero behind.
 // Each wave's device-coherent stores are acknowledged before.
-__device__ __forceinline__ bool arrive(SelectShared &sh, uint32_t *counter, int n) {
+template <int MAXW>
+__device__ __forceinline__ bool arrive(SelectShared<MAXW> &sh, uint32_t *counter, int n) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -210,40 +242,30 @@ __device__ __forceinline__ bool arrive(SelectShared &sh, uint32_t *counter, int 
   return sh.last != 0;
 }
 
-// log(sum of exp) of a row from its chunks' (max, sum), a lane each.
-__device__ __forceinline__ double log_sum(f32x2 st) {
-  const float top = wave_max(st.x);
-  double sum = st.x > -INFINITY ? (double)st.y * exp((double)st.x - (double)top) : 0.0;
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const u64 u = __builtin_bit_cast(u64, sum);
-    const u64 o = ((u64)(uint32_t)__shfl_xor((int)(u >> 32), d, 64) << 32) |
-                  (uint32_t)__shfl_xor((int)(uint32_t)u, d, 64);
-    sum += __builtin_bit_cast(double, o);
-  }
-  return top > -INFINITY ? (double)top + log(sum) : 0.0;
+// A row's sum of exp from its chunks' (max, sum), a lane each: (exponent, sum).
+__device__ __forceinline__ void join_sums(f32x2 st, double *e, double *sum) {
+  const float top = across16<true>(across4(st.x));
+  *e = exponent(top);
+  *sum = wave_total(st.x > -INFINITY ? (double)st.y * (double)shift(st.x, top) : 0.0);
+}
+__device__ __forceinline__ double log_sum(double e, double sum) {
+  return sum > 0.0 ? (e + log2(sum)) / (double)kLog2e : 0.0;
 }
 
-// A candidate of a group.  Order: the score, then the lower beam, then the key.
-struct Entry {
-  double score;
-  u64 key;
-  int beam, pad;
-};
-static_assert(sizeof(Entry) * kFlat <= 8 * kCandidates, "all candidates may tie");
-
-// The W best of the group's candidates: entry(j) of this thread, j < N, at a
-// score of NaN none.  A bound that W scores reach, then ranks by counting among
-// those that do.  Ends with winner r in best[r].
-template <int N, typename Get>
-__device__ __forceinline__ void select_group(SelectShared &sh, int W, const double (&score)[N],
-                                             Get entry, int *best) {
+// The W best of the group's candidates, this thread's being score, key and beam
+// [j], j < N, where the key is not 0; ordered by score, then the lower beam, then
+// the larger key.  A bound that W scores reach, then ranks by counting among
+// those that do.  Ends with winner r in sh.winner[r].
+template <int N, int MAXW>
+__device__ __forceinline__ void select_group(SelectShared<MAXW> &sh, int W,
+                                             const double (&score)[N], const u64 (&key)[N],
+                                             const int (&beam)[N]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   Entry *list = reinterpret_cast<Entry *>(sh.cand);
   u64 mine = 0;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const u64 k = score[j] == score[j] ? order_of(score[j]) : 0;
+    const u64 k = key[j] != 0 ? order_of(score[j]) : 0;
     mine = k > mine ? k : mine;
   }
   const u64 b = wave_bound(mine, W);
@@ -255,25 +277,33 @@ __device__ __forceinline__ void select_group(SelectShared &sh, int W, const doub
   for (int w = 0; w < kWaves; ++w) bound = sh.bound[0][w] > bound ? sh.bound[0][w] : bound;
 #pragma unroll
   for (int j = 0; j < N; ++j)
-    if (score[j] == score[j] && order_of(score[j]) >= bound)
-      list[atomicAdd(&sh.count, 1u)] = entry(j);
+    if (key[j] != 0 && order_of(score[j]) >= bound) {
+      const uint32_t at = atomicAdd(&sh.count, 1u);
+      list[at] = Entry{score[j], key[j]};
+      sh.beam[at] = (uint8_t)beam[j];
+    }
   __syncthreads();
   const int all = sh.count;
   for (int i = tid; i < all; i += kThreads) {
     const Entry e = list[i];
+    const int w = sh.beam[i];
     int r = 0;
+#pragma unroll 4
     for (int c = 0; c < all; ++c) {
       const Entry u = list[c];
-      const bool before = u.beam != e.beam ? u.beam < e.beam : u.key > e.key;
-      r += u.score > e.score || (u.score == e.score && before) ? 1 : 0;
+      bool before = u.score > e.score;
+      if (u.score == e.score) before = sh.beam[c] != w ? sh.beam[c] < w : u.key > e.key;
+      r += before ? 1 : 0;
     }
-    if (r < W) best[r] = i;
+    if (r < W) sh.winner[r] = i;
   }
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, SelectPlan p) {
-  __shared__ SelectShared sh;
+template <int MAXW>
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8)))
+select_kernel(SelectArgs a, SelectPlan p) {
+  __shared__ SelectShared<MAXW> sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int chunk = blockIdx.x, row = blockIdx.y, W = a.W;
   const bool finished = a.finished_in && a.finished_in[row] != 0;
@@ -288,63 +318,85 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, SelectPl
     const int64_t i0 = (int64_t)chunk * p.tiles * kTile + 4 * tid;
     const int64_t stop = min((int64_t)a.V, (int64_t)(chunk + 1) * p.tiles * kTile);
     f32x4 next[kQuads];
+    // The last tile of a row checks every logit; the others go out together and
+    // stay in flight while the tile before them is worked on.
     auto load = [&](int64_t at) {
+      const int64_t last = at - 4 * tid + kTile;
+      if (last <= stop) {
 #pragma unroll
-      for (int j = 0; j < kQuads; ++j) {
-        const int64_t i = at + j * 4 * kThreads;
-        if (i + 4 <= stop) {
-          next[j] = *(const BITNET_GLOBAL f32x4_row *)(x + i);
-        } else {
+        for (int j = 0; j < kQuads; ++j)
+          next[j] = __builtin_nontemporal_load(
+              (const BITNET_GLOBAL f32x4_row *)(x + at + j * 4 * kThreads));
+      } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) next[j][e] = i + e < stop ? ld_global<float>(x + i + e) : NAN;
-        }
+        for (int j = 0; j < kQuads; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int64_t i = at + j * 4 * kThreads + e;
+            next[j][e] = i < stop ? ld_global<float>(x + i) : NAN;
+          }
       }
     };
     load(i0);
+    // Sum of exp(x - m), m the running maximum, as exp2(x c - fl(m c)): one fma
+    // and one exp2 a logit, and since the join takes the same fl(m c), its
+    // rounding cancels.  (Where m c would overflow: exp2((x - m) c).)
     float m = -INFINITY, s = 0.0f;
     for (int tile = 0; tile < p.tiles; ++tile) {
       const int64_t at = i0 + (int64_t)tile * kTile;
+      // (Held back: the compiler would otherwise move the first use of each logit
+      // up behind its load, into the tile before, and wait for it there.)
+#pragma unroll
+      for (int j = 0; j < kQuads; ++j) asm volatile("" : "+v"(next[j]));
       float v[kPer];
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) v[j] = clean(next[j >> 2][j & 3]);
+      for (int j = 0; j < kPer; ++j) v[j] = fmaxf(next[j >> 2][j & 3], -INFINITY);   // NaN: -inf
       if (tile + 1 < p.tiles) load(at + kTile);
-      // The thread's largest: ties go to the first, which has the lower token.
       float top = v[0];
-      int where = 0;
 #pragma unroll
-      for (int j = 1; j < kPer; ++j)
-        if (v[j] > top) {
-          top = v[j];
-          where = j;
-        }
-      auto token = [&](int j) { return at + (j >> 2) * 4 * kThreads + (j & 3); };
-      const u64 mine = at < stop ? key_of(top, (uint32_t)token(where)) : 0;
+      for (int j = 1; j < kPer; ++j) top = fmaxf(top, v[j]);
+      if (__any(top == INFINITY)) {
+        top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) top = fmaxf(top, v[j] = clean(v[j]));
+      }
       const float m_new = fmaxf(m, top);
       if (m_new > -INFINITY) {
         float e[kPer];
+        const float mc = m_new * kLog2e;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) e[j] = __expf(v[j] - m_new);
+        for (int j = 0; j < kPer; ++j)
+          e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[j], kLog2e, -mc));
+        if (huge(m_new))
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) e[j] = __builtin_amdgcn_exp2f((v[j] - m_new) * kLog2e);
 #pragma unroll
         for (int d = kPer / 2; d > 0; d >>= 1)
 #pragma unroll
           for (int j = 0; j < d; ++j) e[j] += e[j + d];
-        s = s * __expf(m - m_new) + e[0];
+        s = s * shift(m, m_new) + e[0];
         m = m_new;
       }
-      select_largest<kPer>(sh, W, tile ? W : 0, tile & 1, mine, [&](int j) {
-        return token(j) < stop ? key_of(v[j], (uint32_t)token(j)) : 0;
-      });
+      auto token = [&](int j) { return at + (j >> 2) * 4 * kThreads + (j & 3); };
+      select_largest<kPer>(
+          sh, W, tile ? W : 0, tile & 1, tile == 0 || top >= logit_of(sh.best[W - 1]),
+          [&]() {   // ties: the first of the thread's, which has the lowest token
+            int where = kPer - 1;
+#pragma unroll
+            for (int j = kPer - 2; j >= 0; --j) where = v[j] == top ? j : where;
+            return at < stop ? key_of(top, (uint32_t)token(where)) : 0;
+          },
+          [&](int j) { return token(j) < stop ? key_of(v[j], (uint32_t)token(j)) : 0; });
     }
     // The chunk's maximum and sum.
-    const float top = wave_max(m);
+    const float top = across16<true>(across4(m));
     if (lane == 0) sh.m[wave] = top;
     __syncthreads();
     float all = sh.m[0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) all = fmaxf(all, sh.m[w]);
-    s = all > -INFINITY ? s * __expf(m - all) : 0.0f;
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d, 64);
+    s = all > -INFINITY ? s * shift(m, all) : 0.0f;
+    s = across16<false>(sum4(s));
     if (lane == 0) sh.s[wave] = s;
     __syncthreads();
     if (tid < W) st_device(keys + chunk * W + tid, sh.best[tid]);
@@ -354,8 +406,6 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, SelectPl
   }
   const int beam = row % W, g0 = row - beam;
   uint32_t *group = counters + kRowCounters + row / W;
-  __shared__ int winner[kMaxWidth];
-  __shared__ double lse[kMaxWidth];
   // A finished beam's candidates: eos at the unchanged score, then the other
   // tokens from the lowest.
   auto finished_key = [&](int i) {
@@ -365,47 +415,60 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, SelectPl
 
   if (p.flat) {
     if (!arrive(sh, group, W * p.chunks)) return;
-    for (int w = wave; w < W; w += kWaves) {
-      const f32x2 *row_stats = reinterpret_cast<f32x2 *>(a.ws + p.stats) + (int64_t)(g0 + w) * p.chunks;
-      f32x2 st = {-INFINITY, 0.0f};
-      if (lane < p.chunks && !(a.finished_in && a.finished_in[g0 + w] != 0))
-        st = __builtin_bit_cast(f32x2, ld_device(row_stats + lane));
-      const double v = log_sum(st);
-      if (lane == 0) lse[w] = v;
-    }
+    // Everything is asked for at once: keys, flags, scores, and a wave per row
+    // its sums.
     constexpr int kN = (kFlat + kThreads - 1) / kThreads;
+    constexpr int kRows = (MAXW + kWaves - 1) / kWaves;
     const int each = p.chunks * W;
+    const float per_each = __builtin_amdgcn_rcpf((float)each);
     const u64 *all_keys = reinterpret_cast<const u64 *>(a.ws + p.keys) + (int64_t)g0 * each;
     u64 k[kN];
     int of[kN];
-    double base[kN], score[kN];
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const int i = tid + j * kThreads;
-      k[j] = 0;
-      of[j] = 0;
-      if (i < W * each) {
-        of[j] = i / each;
-        const int place = i - of[j] * each;
-        base[j] = (double)clean(a.scores_in[g0 + of[j]]);
-        if (a.finished_in && a.finished_in[g0 + of[j]] != 0) {
-          k[j] = place < W ? finished_key(place) : 0;
-          if (place != 0) base[j] = -INFINITY;
-          of[j] |= 0x100;
-        } else {
-          k[j] = ld_device(all_keys + i);
-        }
-      }
+      k[j] = i < W * each ? ld_device(all_keys + i) : 0;
+      of[j] = i < W * each ? (int)(((float)i + 0.5f) * per_each) : 0;   // exact: i < 2^10
     }
+    if (tid < W) {
+      sh.from[tid] = clean(a.scores_in[g0 + tid]);
+      sh.flag[tid] = a.finished_in && a.finished_in[g0 + tid] != 0;
+    }
+    double exps = 0.0, sums = 0.0;   // of row wave + kWaves * lane
+    f32x2 st[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int w = wave + r * kWaves;
+      st[r] = f32x2{-INFINITY, 0.0f};
+      if (w < W && lane < p.chunks)
+        st[r] = __builtin_bit_cast(
+            f32x2, ld_device(reinterpret_cast<f32x2 *>(a.ws + p.stats) +
+                             (int64_t)(g0 + w) * p.chunks + lane));
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      double e, sum;
+      join_sums(st[r], &e, &sum);
+      exps = lane == r ? e : exps;
+      sums = lane == r ? sum : sums;
+    }
+    const double v = log_sum(exps, sums);
+    if (lane < kRows && wave + lane * kWaves < W) sh.lse[wave + lane * kWaves] = v;
     __syncthreads();
+    double score[kN];
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
-      score[j] = NAN;
-      if (k[j] != 0)
-        score[j] = of[j] & 0x100 ? base[j] : base[j] + ((double)logit_of(k[j]) - lse[of[j]]);
+      const int i = tid + j * kThreads;
+      const double base = (double)sh.from[of[j]];
+      if (sh.flag[of[j]] != 0) {
+        const int place = i - of[j] * each;
+        k[j] = i < W * each && place < W ? finished_key(place) : 0;
+        score[j] = place == 0 ? base : (double)-INFINITY;
+      } else {
+        score[j] = base + ((double)logit_of(k[j]) - sh.lse[of[j]]);
+      }
     }
-    select_group<kN>(sh, W, score, [&](int j) { return Entry{score[j], k[j], of[j] & 0xff, 0}; },
-                     winner);
+    select_group<kN>(sh, W, score, k, of);
   } else {
     if (!arrive(sh, counters + row, p.chunks)) return;
     // The row: its W largest keys and their scores.
@@ -429,41 +492,48 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, SelectPl
         mine = k[j] > mine ? k[j] : mine;
       }
       if (wave == 0) {   // the chunks are lanes of the first wave
-        const double v = log_sum(st);
-        if (lane == 0) lse[0] = v;
+        double e, sum;
+        join_sums(st, &e, &sum);
+        const double v = log_sum(e, sum);
+        if (lane == 0) sh.lse[0] = v;
       }
-      select_largest<kJoinPer>(sh, W, 0, 0, mine, [&](int j) { return k[j]; });
+      select_largest<kJoinPer>(sh, W, 0, 0, true, [&]() { return mine; },
+                               [&](int j) { return k[j]; });
       if (tid < W) {
         const u64 key = sh.best[tid];
-        const double t = base + ((double)logit_of(key) - lse[0]);
+        const double t = base + ((double)logit_of(key) - sh.lse[0]);
         st_device(scores + (int64_t)row * W + tid, __builtin_bit_cast(u64, t));
         st_device(row_keys + (int64_t)row * W + tid, key);
       }
     }
     if (!arrive(sh, group, W)) return;
-    constexpr int kN = kMaxWidth * kMaxWidth / kThreads;
+    constexpr int kN = (MAXW * MAXW + kThreads - 1) / kThreads;
     double score[kN];
+    u64 k[kN];
+    int of[kN];
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const int i = tid + j * kThreads;
-      score[j] = i < W * W ? __builtin_bit_cast(double, ld_device(scores + (int64_t)g0 * W + i)) : NAN;
+      score[j] = 0.0;
+      k[j] = 0;
+      of[j] = 0;
+      if (i < W * W) {
+        score[j] = __builtin_bit_cast(double, ld_device(scores + (int64_t)g0 * W + i));
+        k[j] = ld_device(row_keys + (int64_t)g0 * W + i);
+        of[j] = i / W;
+      }
     }
-    select_group<kN>(
-        sh, W, score,
-        [&](int j) {
-          const int i = tid + j * kThreads;
-          return Entry{score[j], ld_device(row_keys + (int64_t)g0 * W + i), i / W, 0};
-        },
-        winner);
+    select_group<kN>(sh, W, score, k, of);
   }
 
   // finished_out may be finished_in, scores_out scores_in: every row of the
   // group has read its own, and here flags are read before any is written.
-  int fin = 0;
-  Entry e = {0.0, 0, 0, 0};
+  int fin = 0, from_beam = 0;
+  Entry e = {0.0, 0};
   if (tid < W) {
-    e = reinterpret_cast<const Entry *>(sh.cand)[winner[tid]];
-    if (a.finished_in) fin = a.finished_in[g0 + e.beam] != 0;
+    e = reinterpret_cast<const Entry *>(sh.cand)[sh.winner[tid]];
+    from_beam = sh.beam[sh.winner[tid]];
+    if (a.finished_in) fin = a.finished_in[g0 + from_beam] != 0;
   }
   __syncthreads();
   if (tid < W) {
@@ -471,7 +541,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(SelectArgs a, SelectPl
     const int token = (int)token_of(e.key);
     a.scores_out[o] = (float)e.score;
     a.tokens[o] = token;
-    a.parents[o] = g0 + e.beam;
+    a.parents[o] = g0 + from_beam;
     if (a.finished_in) a.finished_out[o] = fin || token == a.eos;
   }
 }
@@ -484,7 +554,11 @@ size_t select_workspace_bytes(int64_t B, int64_t W, int64_t V) {
 
 hipError_t launch_beam_select(const SelectArgs &a, hipStream_t stream) {
   const SelectPlan p = select_plan((int64_t)a.B * a.W, a.W, a.V);
-  select_kernel<<<dim3(p.chunks, a.B * a.W), kThreads, 0, stream>>>(a, p);
+  const dim3 grid(p.chunks, a.B * a.W);
+  if (a.W <= kNarrow)
+    select_kernel<kNarrow><<<grid, kThreads, 0, stream>>>(a, p);
+  else
+    select_kernel<kMaxWidth><<<grid, kThreads, 0, stream>>>(a, p);
   return hipGetLastError();
 }
 
