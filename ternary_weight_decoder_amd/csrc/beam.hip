@@ -40,12 +40,11 @@ constexpr int kMaxChunks = 64;                       // of a row
 constexpr int kJoinPer = kMaxChunks * kMaxWidth / kThreads;
 constexpr int kRowCounters = kMaxRows;               // then one counter per group
 constexpr int kHeaderBytes = 2 * 4 * kMaxRows;
-// Workgroups wanted before a workgroup takes more than one tile: two rounds of
-// eight a compute unit (256 rows of 151,936 logits: see below).
-#ifndef BITNET_SELECT_GROUPS
-#define BITNET_SELECT_GROUPS 1024
-#endif
-constexpr int kTargetGroups = BITNET_SELECT_GROUPS;
+// Workgroups before a workgroup takes more than one tile: four a compute unit, as
+// many as its registers hold.  256 rows of 151,936 logits: 44 us, as with 1536;
+// 2048 take 49, 512 take 58.  One group of 32 such rows: 40 us, 55 with 1536.
+constexpr int kTargetGroups = 1024;
+constexpr int kSimdWaves = 4;
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 // Rows are only 4-byte aligned.
@@ -98,10 +97,9 @@ __device__ __forceinline__ float shift(float m, float n) {
 __device__ __forceinline__ double exponent(float m) {
   return huge(m) ? (double)m * (double)kLog2e : (double)(m * kLog2e);
 }
-// The bits of a score in unsigned order; above 0 (a score is never NaN).
-__device__ __forceinline__ u64 order_of(double t) {
-  const u64 b = __builtin_bit_cast(u64, t + 0.0);
-  return b ^ ((b >> 63) ? ~0ull : 1ull << 63);
+// The bits of a rounded score in unsigned order; above 0 (a score is never NaN).
+__device__ __forceinline__ uint32_t order_of(double t) {
+  return (uint32_t)(key_of((float)t, 0) >> 32);
 }
 __device__ __forceinline__ uint32_t token_of(u64 key) { return 0xffffffffu - (uint32_t)key; }
 
@@ -140,36 +138,41 @@ struct SelectShared {
   uint8_t beam[kEntries];              // of the entries
 };
 
-// A bound that W lanes' keys reach, and no more than W unless keys are equal
-// (0 where fewer than W lanes have one): the W-th largest key from the top bit
-// down, until exactly W lanes are left above.
-__device__ __forceinline__ u64 wave_bound(u64 key, int W) {
-  const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
+// The largest prefix v of bits, from the top two at a time, that the keys of W
+// lanes reach, until no more than `most` lanes do; `at` lanes do in the end, `above`
+// of those counted elsewhere.
+__device__ __forceinline__ uint32_t bound_bits(uint32_t key, bool in, int above, int W, int most,
+                                               int *at) {
   uint32_t v = 0;
-  int at = 64;
 #pragma unroll 1
-  for (int top = 31; top >= 0 && at != W; top -= 8)
+  for (int top = 30; top >= 0 && *at > most; top -= 4)
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      const uint32_t t = v | (1u << (top - b));
-      const int n = __builtin_popcountll(__ballot(hi >= t));
-      v = n >= W ? t : v;
-      at = n >= W ? n : at;
-    }
-  if (v == 0) return 0;
-  uint32_t low = 0;
-  if (at != W) {   // lanes share the value
-    const int above = __builtin_popcountll(__ballot(hi > v));
-#pragma unroll 1
-    for (int b = 31; b >= 0 && at != W; --b) {
-      const uint32_t t = low | (1u << b);
-      const int n = above + __builtin_popcountll(__ballot(hi == v && lo >= t));
-      if (n >= W) {
-        low = t;
-        at = n;
+    for (int b = 0; b < 4; b += 2) {
+      uint32_t t[3];
+      int n[3];
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        t[q] = v | ((uint32_t)(q + 1) << (top - b));
+        n[q] = above + __builtin_popcountll(__ballot(in && key >= t[q]));
+      }
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        v = n[q] >= W ? t[q] : v;
+        *at = n[q] >= W ? n[q] : *at;
       }
     }
-  }
+  return v;
+}
+// A bound that W lanes' keys reach, and no more than `most` >= W lanes' unless
+// keys are equal (0 where fewer than W lanes have one).
+__device__ __forceinline__ u64 wave_bound(u64 key, int W, int most) {
+  const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
+  int at = 64;
+  const uint32_t v = bound_bits(hi, true, 0, W, most, &at);
+  if (v == 0) return 0;
+  uint32_t low = 0;
+  if (at > most)   // lanes share the value
+    low = bound_bits(lo, hi == v, __builtin_popcountll(__ballot(hi > v)), W, most, &at);
   return ((u64)v << 32) | low;
 }
 
@@ -190,7 +193,7 @@ __device__ __forceinline__ void select_largest(SelectShared<MAXW> &sh, int W, in
     above = __builtin_popcountll(__ballot(mine > floor));
     // A wave with few keys above what is there already needs no further bound:
     // MAXW lanes of a wave fit the list.
-    if (above > (have ? MAXW : W)) b = wave_bound(mine, W);
+    if (above > (have ? MAXW : W)) b = wave_bound(mine, W, MAXW);
   }
   if (lane == 0) {
     sh.bound[flip][wave] = b;
@@ -254,7 +257,8 @@ __device__ __forceinline__ double log_sum(double e, double sum) {
 
 // The W best of the group's candidates, this thread's being score, key and beam
 // [j], j < N, where the key is not 0; ordered by score, then the lower beam, then
-// the larger key.  A bound that W scores reach, then ranks by counting among
+// the larger key.  A bound that W scores reach, both rounded to fp32 (which keeps
+// the order: whatever is below it is below W others), then ranks by counting among
 // those that do.  Ends with winner r in sh.winner[r].
 template <int N, int MAXW>
 __device__ __forceinline__ void select_group(SelectShared<MAXW> &sh, int W,
@@ -262,13 +266,14 @@ __device__ __forceinline__ void select_group(SelectShared<MAXW> &sh, int W,
                                              const int (&beam)[N]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   Entry *list = reinterpret_cast<Entry *>(sh.cand);
-  u64 mine = 0;
+  uint32_t mine = 0, order[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const u64 k = key[j] != 0 ? order_of(score[j]) : 0;
-    mine = k > mine ? k : mine;
+    order[j] = key[j] != 0 ? order_of(score[j]) : 0;
+    mine = max(mine, order[j]);
   }
-  const u64 b = wave_bound(mine, W);
+  int at = 64;
+  const uint32_t b = bound_bits(mine, true, 0, W, W, &at);
   if (lane == 0) sh.bound[0][wave] = b;
   if (tid == 0) sh.count = 0;
   __syncthreads();
@@ -277,7 +282,7 @@ __device__ __forceinline__ void select_group(SelectShared<MAXW> &sh, int W,
   for (int w = 0; w < kWaves; ++w) bound = sh.bound[0][w] > bound ? sh.bound[0][w] : bound;
 #pragma unroll
   for (int j = 0; j < N; ++j)
-    if (key[j] != 0 && order_of(score[j]) >= bound) {
+    if (order[j] >= bound) {
       const uint32_t at = atomicAdd(&sh.count, 1u);
       list[at] = Entry{score[j], key[j]};
       sh.beam[at] = (uint8_t)beam[j];
@@ -301,7 +306,7 @@ __device__ __forceinline__ void select_group(SelectShared<MAXW> &sh, int W,
 }
 
 template <int MAXW>
-__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8)))
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kSimdWaves)))
 select_kernel(SelectArgs a, SelectPlan p) {
   __shared__ SelectShared<MAXW> sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
