@@ -1,6 +1,8 @@
 // The paged key-value cache: the page map of a step, the write of new tokens
 // and the reordering of beams.  (The attention that reads the cache is in
 // attention.hip.)
+#include <algorithm>
+
 #include "bitnet_device.hpp"
 #include "bitnet_internal.hpp"
 #include "kv.hpp"
@@ -14,89 +16,163 @@ namespace {
 // Two running sums over the requests decide who is granted (pages needed and
 // tokens added, over the requests that fit their tables), two more over the
 // granted ones give each its first page and first token.  One workgroup does
-// all of it, so that nothing but its own barriers orders the steps.
+// all of it, so that nothing but its own barriers orders the steps; what bounds
+// it is their latency.  So each pair of sums is one pass of saturating adds in
+// registers and one barrier; pages given back and granted are moved a thread
+// each, which finds its request by bisection of the sums; and the top of the
+// stack is asked for at the start, for the calls in which no request ends.
+// Steps of many tokens write their slots in a second kernel of many workgroups.
 // ---------------------------------------------------------------------------
 
 constexpr int kMapThreads = 1024;
 constexpr int kMapWaves = kMapThreads / 64;
 
-__device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
-  const int lo = __shfl_up((int)(uint32_t)v, d, 64);
-  const int hi = __shfl_up((int)(v >> 32), d, 64);
-  return ((int64_t)hi << 32) | (uint32_t)lo;
+struct Pair {
+  uint32_t p, t;   // pages, tokens
+};
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) {
+  return __builtin_elementwise_add_sat(a, b);
+}
+__device__ __forceinline__ Pair add_sat(Pair a, Pair b) {
+  return {add_sat(a.p, b.p), add_sat(a.t, b.t)};
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ Pair scan_step(Pair v) {
+  return add_sat(v, Pair{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)v.p, CTRL, ROWS, 0xF, false),
+                         (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v.t, CTRL, ROWS, 0xF, false)});
+}
+// Inclusive sums over the rows of 16 lanes.
+__device__ __forceinline__ Pair row_scan(Pair v) {
+  v = scan_step<0x111, 0xF>(v);   // row_shr:1
+  v = scan_step<0x112, 0xF>(v);
+  v = scan_step<0x114, 0xF>(v);
+  return scan_step<0x118, 0xF>(v);
+}
+__device__ __forceinline__ Pair lane_of(Pair v, int lane) {
+  return {(uint32_t)__builtin_amdgcn_readlane((int)v.p, lane),
+          (uint32_t)__builtin_amdgcn_readlane((int)v.t, lane)};
 }
 
-// Inclusive sum over the workgroup's threads, plus the total in *total.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *wave_sums, int64_t *total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t u = shfl_up64(v, d);
-    if (lane >= d) v += u;
-  }
-  if (lane == 63) wave_sums[wave] = v;
+// Inclusive sums over the workgroup's threads, which saturate (and so stay above
+// whatever they are compared with), and the total.  Calls in a row take different
+// rows of `sums`: one barrier then orders them.
+__device__ __forceinline__ Pair block_scan(Pair v, Pair *sums, Pair *total) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  v = row_scan(v);
+  v = scan_step<0x142, 0xA>(v);   // row_bcast:15
+  v = scan_step<0x143, 0xC>(v);   // row_bcast:31
+  if (lane == 63) sums[wave] = v;
   __syncthreads();
-  int64_t before = 0, all = 0;
-  for (int w = 0; w < kMapWaves; ++w) {
-    const int64_t s = wave_sums[w];
-    before += w < wave ? s : 0;
-    all += s;
-  }
-  *total = all;
-  __syncthreads();
-  return v + before;
+  Pair w = {0, 0};
+  if (lane < (int)(blockDim.x >> 6)) w = sums[lane];
+  w = row_scan(w);
+  *total = lane_of(w, kMapWaves - 1);
+  return wave ? add_sat(v, lane_of(w, wave - 1)) : v;
 }
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
-// Token t of the step: its request by bisection of starts, its position from
-// the request's length after the step, its slot from the table.
-__device__ __forceinline__ void map_token(const KvMapArgs &a, const int32_t *starts,
-                                          const int32_t *lens_after, int64_t t) {
-  int slot = -1, pos = -1, row = -1;
-  if (t < starts[a.B]) {
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {   // the last request that starts at or before t
-      const int mid = (lo + hi + 1) >> 1;
-      if (starts[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    row = lo;
-    pos = lens_after[row] - (starts[row + 1] - (int)t);
-    const int page = a.tables[(int64_t)row * a.max_pages + (pos >> a.page_shift)];
-    if (page >= 0 && page < a.pages)
-      slot = (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+// The first i < n with ends[i] > k; the last of them is above k.
+__device__ __forceinline__ int find(const uint32_t *ends, int n, uint32_t k) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] > k) hi = mid; else lo = mid + 1;
   }
-  a.slots[t] = slot;
-  a.positions[t] = pos;
-  a.rows[t] = row;
+  return lo;
+}
+
+// Tokens t0 + j * step of the step, j < N: the request by bisection of starts, the
+// position from the request's length after the step, the slot from the table.
+template <int N>
+__device__ __forceinline__ void map_tokens(const KvMapArgs &a, const int32_t *starts,
+                                           const int32_t *lens_after, int64_t t0, int step) {
+  int lo[N], hi[N], pos[N], page[N];
+  const int all = starts[a.B];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    lo[j] = 0;
+    hi[j] = a.B - 1;
+  }
+  for (int n = a.B - 1; n > 0; n >>= 1)   // the last request that starts at or before t
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int mid = (lo[j] + hi[j] + 1) >> 1;
+      const bool up = starts[mid] <= t0 + j * step;
+      lo[j] = up ? mid : lo[j];
+      hi[j] = up ? hi[j] : max(mid - 1, lo[j]);
+    }
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int64_t t = t0 + j * step;
+    pos[j] = page[j] = -1;
+    if (t < all) {
+      pos[j] = lens_after[lo[j]] - (starts[lo[j] + 1] - (int)t);
+      page[j] = a.tables[(int64_t)lo[j] * a.max_pages + (pos[j] >> a.page_shift)];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int64_t t = t0 + j * step;
+    if (t < a.T) {
+      const bool there = page[j] >= 0 && page[j] < a.pages;
+      a.slots[t] =
+          there ? (page[j] << a.page_shift) + (pos[j] & ((1 << a.page_shift) - 1)) : -1;
+      a.positions[t] = pos[j];
+      a.rows[t] = t < all ? lo[j] : -1;
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(KvMapArgs a, int tokens_here) {
-  __shared__ int64_t sums[kMapWaves];
+  __shared__ Pair sums[2][kMapWaves];
+  __shared__ uint32_t ends[kMapThreads];
+  __shared__ int32_t firsts[kMapThreads], helds[kMapThreads];
   __shared__ int32_t starts[kMaxRows + 1];
   __shared__ int32_t lens_after[kMaxRows];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
   const int ps = 1 << a.page_shift;
   const int cap = a.max_pages << a.page_shift;   // tokens a table holds
-  int64_t total;
+  int flip = 0;
+  Pair total;
+
+  const int height0 = clampi(a.state_in[2 * a.B], 0, a.pages);
+  const int top = tid < height0 ? a.free_pages[height0 - 1 - tid] : 0;
 
   // Ended requests give their pages back.
-  int64_t height = clampi(a.state_in[2 * a.B], 0, a.pages);
-  for (int b0 = 0; b0 < a.B; b0 += kMapThreads) {
-    const int r = b0 + tid;
-    const bool ends = r < a.B && a.new_lens[r] < 0;
-    const int held = ends ? clampi(a.state_in[a.B + r], 0, a.max_pages) : 0;
-    const int64_t at = height + block_scan(held, sums, &total) - held;
-    for (int i = 0; i < held; ++i)
-      if (at + i < a.pages) a.free_pages[at + i] = a.owned[(int64_t)r * a.max_pages + i];
-    height = min(height + total, (int64_t)a.pages);
+  int height = height0;
+  for (int b0 = 0; b0 < a.B; b0 += threads) {
+    const int r = b0 + tid, rows = min(threads, a.B - b0);
+    const bool ends_here = r < a.B && a.new_lens[r] < 0;
+    const int held = ends_here ? clampi(a.state_in[a.B + r], 0, a.max_pages) : 0;
+    const Pair upto = block_scan({(uint32_t)held, 0}, sums[flip ^= 1], &total);
+    if (total.p == 0) continue;   // the same for every thread
+    ends[tid] = upto.p;
+    __syncthreads();
+    const uint32_t n = min(total.p, (uint32_t)(a.pages - height));
+    for (uint32_t k0 = tid; k0 < n; k0 += 4 * threads) {
+      int page[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t k = k0 + j * threads;
+        if (k < n) {
+          const int q = find(ends, rows, k);
+          page[j] = a.owned[(int64_t)(b0 + q) * a.max_pages + (k - (q ? ends[q - 1] : 0))];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (k0 + j * threads < n) a.free_pages[height + k0 + j * threads] = page[j];
+    }
+    height += n;
   }
-  __syncthreads();   // the stack is read below
+  const bool untouched = height == height0;   // else the stack is read below
+  if (!untouched) __syncthreads();
 
-  int64_t want_pages = 0, want_tokens = 0;   // of the requests before this chunk
-  int64_t page0 = 0, token0 = 0;             // granted before this chunk
-  for (int b0 = 0; b0 < a.B; b0 += kMapThreads) {
-    const int r = b0 + tid;
+  Pair want = {0, 0}, granted = {0, 0};   // of the requests before this chunk
+  for (int b0 = 0; b0 < a.B; b0 += threads) {
+    const int r = b0 + tid, rows = min(threads, a.B - b0);
     int len = 0, held = 0, add = 0;
     if (r < a.B) {
       const int n = a.new_lens[r];
@@ -110,50 +186,81 @@ __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(KvMapArgs a, int to
     const int64_t after = (int64_t)len + add;
     const int64_t need64 = ((after + ps - 1) >> a.page_shift) - first;
     const bool fits = after <= cap && held + need64 <= a.max_pages;
-    const int64_t need = fits ? need64 : 0;
-    const int64_t upto_p = want_pages + block_scan(need, sums, &total);
-    want_pages += total;
-    const int64_t upto_t = want_tokens + block_scan(fits ? add : 0, sums, &total);
-    want_tokens += total;
-    const bool paged = need == 0 || upto_p <= height;
-    const bool room = add == 0 || upto_t <= a.T;
+    const uint32_t need = fits ? (uint32_t)need64 : 0;
+    const Pair upto = add_sat(
+        want, block_scan({need, fits ? (uint32_t)add : 0}, sums[flip ^= 1], &total));
+    want = add_sat(want, total);
+    const bool paged = need == 0 || upto.p <= (uint32_t)height;
+    const bool room = add == 0 || upto.t <= a.T;
     const bool ok = fits && paged && room;
-    const int np = ok ? (int)need : 0, nt = ok ? add : 0;
-    const int64_t p_at = page0 + block_scan(np, sums, &total) - np;
-    page0 += total;
-    const int64_t t_at = token0 + block_scan(nt, sums, &total) - nt;
-    token0 += total;
+    const uint32_t np = ok ? need : 0, nt = ok ? (uint32_t)add : 0;
+    // (What is granted is at most the height and T: no sum saturates.)
+    const Pair got = block_scan({np, nt}, sums[flip ^= 1], &total);
+    ends[tid] = got.p;
+    firsts[tid] = first;
+    helds[tid] = held;
     if (r < a.B) {
-      for (int i = 0; i < np; ++i) {
-        const int page = a.free_pages[height - 1 - p_at - i];
-        a.tables[(int64_t)r * a.max_pages + first + i] = page;
-        a.owned[(int64_t)r * a.max_pages + held + i] = page;
-      }
-      starts[r] = (int32_t)t_at;
-      lens_after[r] = len + nt;
-      a.starts[r] = (int32_t)t_at;
+      const int32_t at = (int32_t)(granted.t + got.t - nt);
+      starts[r] = at;
+      lens_after[r] = len + (int)nt;
+      a.starts[r] = at;
       a.status[r] = fits ? (paged ? (room ? 0 : 3) : 2) : 1;
-      a.state_out[r] = len + nt;
-      a.state_out[a.B + r] = held + np;
+      a.state_out[r] = len + (int)nt;
+      a.state_out[a.B + r] = held + (int)np;
     }
+    __syncthreads();
+    const int base = height - 1 - (int)granted.p;
+    const bool have = untouched && granted.p == 0;
+    for (uint32_t k0 = tid; k0 < total.p; k0 += 4 * threads) {
+      int page[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (k0 + j * threads < total.p)
+          page[j] = have && j == 0 && k0 == (uint32_t)tid
+                        ? top
+                        : a.free_pages[base - (int)(k0 + j * threads)];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t k = k0 + j * threads;
+        if (k < total.p) {
+          const int q = find(ends, rows, k);
+          const int i = (int)(k - (q ? ends[q - 1] : 0));
+          const int64_t row = (int64_t)(b0 + q) * a.max_pages;
+          a.tables[row + firsts[q] + i] = page[j];
+          a.owned[row + helds[q] + i] = page[j];
+        }
+      }
+    }
+    granted = add_sat(granted, total);
+    __syncthreads();   // before the lists are written again, and the tables read
   }
   if (tid == 0) {
-    starts[a.B] = (int32_t)token0;
-    a.starts[a.B] = (int32_t)token0;
-    a.state_out[2 * a.B] = (int32_t)(height - page0);
+    starts[a.B] = (int32_t)granted.t;
+    a.starts[a.B] = (int32_t)granted.t;
+    a.state_out[2 * a.B] = height - (int32_t)granted.p;
   }
+  if (!tokens_here) return;
   __syncthreads();
-  if (tokens_here)
-    for (int64_t t = tid; t < a.T; t += kMapThreads) map_token(a, starts, lens_after, t);
+  for (int64_t t = tid; t < a.T; t += 4 * threads) {
+    if (a.T <= threads)
+      map_tokens<1>(a, starts, lens_after, t, threads);
+    else
+      map_tokens<4>(a, starts, lens_after, t, threads);
+  }
 }
 
-__global__ void __launch_bounds__(256) kv_map_tokens_kernel(KvMapArgs a) {
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (t < a.T) map_token(a, a.starts, a.state_out, t);
+constexpr int kTokenThreads = 256, kTokensEach = 4;
+
+__global__ void __launch_bounds__(kTokenThreads) kv_map_tokens_kernel(KvMapArgs a) {
+  __shared__ int32_t starts[kMaxRows + 1];
+  for (int i = threadIdx.x; i <= a.B; i += kTokenThreads) starts[i] = a.starts[i];
+  __syncthreads();
+  const int64_t t = (int64_t)blockIdx.x * kTokenThreads * kTokensEach + threadIdx.x;
+  map_tokens<kTokensEach>(a, starts, a.state_out, t, kTokenThreads);
 }
 
 // Calls of up to this many tokens finish in the one workgroup.
-constexpr int64_t kMapTokensHere = 8192;
+constexpr int64_t kMapTokensHere = 4096;
 
 // ---------------------------------------------------------------------------
 // Append: rotate, convert, scatter.
@@ -270,6 +377,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a) {
 // are disjoint, so one launch copies in place.
 // ---------------------------------------------------------------------------
 
+constexpr int kEach = 4;   // (head, token) pairs of a thread in flight
+
 __global__ void __launch_bounds__(256) beam_reorder_kernel(ReorderArgs a) {
   const int row = blockIdx.x, layer = (int)blockIdx.y - 1;
   const int g0 = row / a.W * a.W, j = row - g0;
@@ -309,23 +418,43 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(ReorderArgs a) {
   if (!move || tail == 0) return;
   const int64_t src = from[last], dst = giver[last];
   if (src < 0 || src >= a.c.pages || dst < 0 || dst >= a.c.pages) return;
-  const int vecs = a.head_dim * a.elem_bytes / 16;   // 16-byte pieces of a token's head
-  const int n = a.c.kv_heads * tail * vecs;
-  for (int side = 0; side < 2; ++side) {
-    uint8_t *base = reinterpret_cast<uint8_t *>(side ? a.c.v : a.c.k) +
-                    layer * a.layer_stride * a.elem_bytes;
-    for (int i = threadIdx.x; i < n; i += 256) {
-      const int piece = i % vecs, tok = i / vecs % tail, h = i / vecs / tail;
-      const int64_t off =
-          (h * a.c.head_stride + tok * a.c.token_stride) * a.elem_bytes + piece * 16;
-      const int64_t pb = a.c.page_stride * a.elem_bytes;
-      st_global<u32x4>(base + dst * pb + off, ld_global<u32x4>(base + src * pb + off));
+  // 16-byte pieces: a thread keeps its piece of a head and steps over (head,
+  // token) pairs, four of them and both sides in flight.
+  const int vec_shift = __builtin_ctz(a.head_dim * a.elem_bytes / 16);
+  const int piece = threadIdx.x & ((1 << vec_shift) - 1);
+  const int step = 256 >> vec_shift, n = a.c.kv_heads * tail;
+  const float per_tail = __builtin_amdgcn_rcpf((float)tail);
+  auto head_of = [&](int m) { return (int)(((float)m + 0.5f) * per_tail); };   // exact: m < 2^18
+  const int64_t page_bytes = a.c.page_stride * a.elem_bytes;
+  const int64_t layer_at = layer * a.layer_stride * a.elem_bytes + piece * 16;
+  uint8_t *k = reinterpret_cast<uint8_t *>(a.c.k) + layer_at;
+  uint8_t *v = reinterpret_cast<uint8_t *>(a.c.v) + layer_at;
+  for (int m0 = threadIdx.x >> vec_shift; m0 < n; m0 += kEach * step) {
+    u32x4 x[2 * kEach];
+    int64_t off[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int m = m0 + j * step;
+      if (m < n) {
+        const int h = head_of(m);
+        off[j] = (h * a.c.head_stride + (m - h * tail) * a.c.token_stride) * a.elem_bytes;
+        x[2 * j] = ld_global<u32x4>(k + src * page_bytes + off[j]);
+        x[2 * j + 1] = ld_global<u32x4>(v + src * page_bytes + off[j]);
+      }
     }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (m0 + j * step < n) {
+        st_global<u32x4>(k + dst * page_bytes + off[j], x[2 * j]);
+        st_global<u32x4>(v + dst * page_bytes + off[j], x[2 * j + 1]);
+      }
+  }
+  for (int side = 0; side < 2; ++side) {
     float *sc = side ? a.c.v_scale : a.c.k_scale;
     if (sc != nullptr) {
       sc += (int64_t)layer * a.c.pages * a.c.kv_heads * ps;
-      for (int i = threadIdx.x; i < a.c.kv_heads * tail; i += 256) {
-        const int tok = i % tail, h = i / tail;
+      for (int i = threadIdx.x; i < n; i += 256) {
+        const int h = head_of(i), tok = i - h * tail;
         sc[(dst * a.c.kv_heads + h) * ps + tok] = sc[(src * a.c.kv_heads + h) * ps + tok];
       }
     }
@@ -336,8 +465,15 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(ReorderArgs a) {
 
 hipError_t launch_kv_map(const KvMapArgs &a, hipStream_t stream) {
   const bool here = a.T <= kMapTokensHere;
-  kv_map_kernel<<<1, kMapThreads, 0, stream>>>(a, here);
-  if (!here) kv_map_tokens_kernel<<<(unsigned)((a.T + 255) / 256), 256, 0, stream>>>(a);
+  // A thread for each request, or for four of the tokens or pages of a table.
+  const int64_t want =
+      std::max<int64_t>({a.B, here ? a.T / 4 : 0, a.max_pages / 4, here && a.T <= 256 ? a.T : 0});
+  const int threads = (int)std::min<int64_t>((want + 63) / 64 * 64, kMapThreads);
+  kv_map_kernel<<<1, threads, 0, stream>>>(a, here);
+  if (!here) {
+    constexpr int kTokens = kTokenThreads * kTokensEach;
+    kv_map_tokens_kernel<<<(unsigned)((a.T + kTokens - 1) / kTokens), kTokenThreads, 0, stream>>>(a);
+  }
   return hipGetLastError();
 }
 
