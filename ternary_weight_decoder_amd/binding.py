@@ -173,8 +173,10 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return _p(s.cuda_stream)
+    if stream is not None:
+        return _p(stream.cuda_stream)
+    # (torch.cuda.current_stream() builds an object: 2.7 us a call against 0.4.)
+    return _p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _dev(t: torch.Tensor, dtype, name: str) -> None:
