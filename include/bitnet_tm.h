@@ -579,7 +579,7 @@ typedef struct bitnet_kv_pool {
  *   in the cache, position in the request, request.  Entries behind the last
  *   token are -1.  slots is -1 too where the table's page is out of range.
  *   Lengths, counts and the stack's height are clamped to their ranges first.
- *   1 <= T < 2^31.  One launch, or two for T > 8192.  No output may overlap
+ *   1 <= T < 2^31.  One launch, or two for T > 4096.  No output may overlap
  *   another array.
  */
 bitnet_status bitnet_kv_map(const bitnet_kv_pool *pool, int64_t T, const int32_t *new_lens,

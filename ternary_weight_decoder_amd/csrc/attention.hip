@@ -173,8 +173,14 @@ struct FragF16 {
     f16x8 u[2];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      u[0][e] = (_Float16)x[e];
-      u[1][e] = (_Float16)(x[e] - (float)u[0][e]);
+      // Pinned: where x is a product the compiler takes the first term once from
+      // the rounded product and, for the difference, once from an fma that
+      // rounds the exact product to fp16 (v_fma_mixlo_f16): next to the middle
+      // between two fp16 numbers they are not the same.
+      float y = x[e];
+      asm("" : "+v"(y));
+      u[0][e] = (_Float16)y;
+      u[1][e] = (_Float16)(y - (float)u[0][e]);
     }
     if constexpr (FOLD) {
       t[0] = second ? u[1] : u[0];
