@@ -78,10 +78,14 @@ constexpr int kFill = 256;         // stretches wanted before they grow beyond a
 constexpr int kShort = 16;
 constexpr int kSingle = 3 * kWaves;   // items up to this are not cut: a join costs three tiles' time
 constexpr int kLine = 8;           // tiles of a stretch that is shared by items, at least
-constexpr int kMaxParts = 128;     // stretches that one item may lie in
+// Parts that are joined at once: the loads of 16 are in flight together.  (One
+// row of 32,767 fp16 tokens: 17.3 us; 21.5 with its 86 parts in one join, of
+// which the join took 8, and longer stretches to keep the parts few.)
+constexpr int kJoined = 16;
+constexpr int kMaxParts = kJoined * kJoined;   // stretches that one item may lie in
 constexpr int kLineRows = 1024;    // rows whose lengths a workgroup sums up itself
 constexpr int kHeaderBytes = 16384;
-static_assert(4 * kGridMany <= kHeaderBytes, "a counter per stretch");
+static_assert(8 * kGridMany <= kHeaderBytes, "two counters per stretch");
 
 // Partial results cross the chip through device-coherent accesses (cache
 // policy sc1), so that no workgroup has to write back or invalidate a cache,
@@ -271,7 +275,7 @@ struct AttendShared {
   __attribute__((aligned(16))) uint8_t tile[kWaves][S::kWaveLds];   // values, then outputs
   float scales[kWaves][2][kTile];      // 8-bit caches: the tile's key and value scales
   float m[kWaves][kHeads], l[kWaves][kHeads], unit[kWaves];
-  float weight[S::kCols][kMaxParts];   // of the joined parts
+  float weight[S::kCols][kJoined];   // of the joined parts
   int32_t start[FEW ? 1 : kLineRows + 1];   // tiles before each row
   int32_t wave_sum[kWaves], wave_max[kWaves];
   uint32_t last;
@@ -754,6 +758,13 @@ attend_kernel(AttendArgs a, AttendGrid g0) {
         a.lse[(int64_t)g.t * a.q_heads + head0 + head] =
             tl > 0.0f ? (tm - kUp + __log2f(tl)) * kLn2 : -INFINITY;
     };
+    auto keep_part = [&](int place, int i, int head, f32x4 sum, float tm, float tl) {
+      st_device(outs, place * kPartBytes + 16 * i, sum);
+      if (i % kQuads == 0)
+        __hip_atomic_store((BITNET_GLOBAL uint64_t *)&stats[place * kHeads + head],
+                           __builtin_bit_cast(uint64_t, f32x2{tm, tl}), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+    };
     for (int i = threadIdx.x; i < n4; i += kThreads) {
       const int head = i / kQuads;
       float tm = sh.m[0][head];
@@ -771,101 +782,110 @@ attend_kernel(AttendArgs a, AttendGrid g0) {
       if (whole) {
         finish(i, head, sum, tm, tl);
       } else {
-        st_device(outs, my_place * kPartBytes + 16 * i, sum);
-        if (i % kQuads == 0)
-          __hip_atomic_store((BITNET_GLOBAL uint64_t *)&stats[my_place * kHeads + head],
-                             __builtin_bit_cast(uint64_t, f32x2{tm, tl}), __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
+        keep_part(my_place, i, head, sum, tm, tl);
       }
     }
 
     if (!whole) {
-      // The last stretch of the item to arrive joins its parts; it leaves the
-      // counter, the first stretch's, at zero.  Each wave's stores have been
-      // acknowledged before the counter moves.
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        uint32_t *ticket = reinterpret_cast<uint32_t *>(a.ws) + w0;
-        const uint32_t n =
-            __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        sh.last = n == (uint32_t)used - 1;
-        if (sh.last) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-      __syncthreads();
-      if (sh.last) {
-        // Part p is at the beginning of stretch w0 + p, unless the item begins
-        // inside its first stretch.
-        const int inside = g.item0 != w0 * stretch ? 1 : 0;
-        auto place_of = [&](int p) { return 2 * (w0 + p) + (p == 0 ? inside : 0); };
-        // Wave w adds up parts w, w + kWaves, ..., a lane per four channels in
-        // each of kWide blocks of the outputs; the loads of kJoin parts go out at
-        // once, the first ones before the weights are known.
-        constexpr int kWide = S::kCols * kQuads / 64;
-        constexpr int kJoin = kWide >= 8 ? 2 : 16 / kWide;
-        f32x4 x[kJoin][kWide], sum[kWide];
-        auto load_parts = [&](int p0) {
-#pragma unroll
-          for (int u = 0; u < kJoin; ++u)
-#pragma unroll
-            for (int b = 0; b < kWide; ++b)
-              x[u][b] = ld_device(outs, place_of(min(p0 + u * kWaves, used - 1)) * kPartBytes +
-                                            16 * min(64 * b + lane, n4 - 1));
-        };
-        load_parts(wave);
-        // A wave per head turns the parts' maxima and sums into weights.
-        for (int head = wave; head < nh; head += kWaves) {
-          f32x2 st[kMaxParts / 64];
-          float tm = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < kMaxParts / 64; ++k) {
-            const int p = lane + 64 * k;
-            st[k] = f32x2{-INFINITY, 0.0f};
-            if (p < used)
-              st[k] = __builtin_bit_cast(
-                  f32x2, (uint64_t)__hip_atomic_load(
-                             (const BITNET_GLOBAL uint64_t *)&stats[place_of(p) * kHeads + head],
-                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-            tm = fmaxf(tm, st[k].x);
+      // The last stretch of the item to arrive joins its parts; with more than
+      // kJoined of them, the last of each group of kJoined joins the group into
+      // its first part's place, and the last of the groups joins those.  Each
+      // leaves its counter at zero: the group's first stretch's (of a group of
+      // two or more, so that no other item begins there), and for the groups the
+      // item's first stretch's among the second counters.  Each wave's stores have
+      // been acknowledged before a counter moves.
+      const int inside = g.item0 != w0 * stretch ? 1 : 0;   // begins inside its first stretch
+      auto place_of = [&](int p) { return 2 * (w0 + p) + (p == 0 ? inside : 0); };
+      uint32_t *counters = reinterpret_cast<uint32_t *>(a.ws) + w0;
+      bool final = used <= kJoined;
+      int first = final ? 0 : ((int)blockIdx.x - w0) & -kJoined;
+      int step = 1, parts = min(kJoined, used - first);
+      uint32_t *ticket = counters + first;
+      for (;;) {
+        if (parts > 1) {
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+          __syncthreads();
+          if (threadIdx.x == 0) {
+            const uint32_t n =
+                __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            sh.last = n == (uint32_t)parts - 1;
+            if (sh.last)
+              __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
           }
-          tm = across16<true>(across4(tm));
-          float tl = 0.0f;
+          __syncthreads();
+          if (!sh.last) break;
+          // Wave w adds up parts w, w + kWaves, ..., a lane per four channels in
+          // each of kWide blocks of the outputs; the loads of kJoin parts go out
+          // at once, the first ones before the weights are known.
+          constexpr int kWide = S::kCols * kQuads / 64;
+          constexpr int kJoin = kWide >= 8 ? 2 : 16 / kWide;
+          f32x4 x[kJoin][kWide], sum[kWide];
+          auto load_parts = [&](int p0) {
 #pragma unroll
-          for (int k = 0; k < kMaxParts / 64; ++k) {
-            const int p = lane + 64 * k;
-            const float f = exp2_fast(st[k].x - (tm == -INFINITY ? 0.0f : tm));
-            tl += st[k].y * f;
-            if (p < used) sh.weight[head][p] = f;
-          }
-          tl = across16<false>(sum4(tl));
-          if (lane == 0) {
-            sh.m[0][head] = tm;
-            sh.l[0][head] = tl;
-          }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int b = 0; b < kWide; ++b) sum[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int p0 = wave; p0 < used; p0 += kJoin * kWaves) {
-          if (p0 != wave) load_parts(p0);
-#pragma unroll
-          for (int u = 0; u < kJoin; ++u)
-            if (p0 + u * kWaves < used)
+            for (int u = 0; u < kJoin; ++u)
 #pragma unroll
               for (int b = 0; b < kWide; ++b)
-                sum[b] += x[u][b] *
-                          sh.weight[min(64 * b + lane, n4 - 1) / kQuads][p0 + u * kWaves];
-        }
+                x[u][b] = ld_device(
+                    outs, place_of(first + step * min(p0 + u * kWaves, parts - 1)) * kPartBytes +
+                              16 * min(64 * b + lane, n4 - 1));
+          };
+          load_parts(wave);
+          // The parts' maxima and sums become weights: four heads a wave, a lane
+          // per part.
+          {
+            const int head = 4 * wave + h;
+            f32x2 st = {-INFINITY, 0.0f};
+            if (c < parts && head < nh)
+              st = __builtin_bit_cast(
+                  f32x2, (uint64_t)__hip_atomic_load(
+                             (const BITNET_GLOBAL uint64_t *)&stats[place_of(first + step * c) *
+                                                                        kHeads + head],
+                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+            const float tm = across16<true>(st.x);
+            const float f = exp2_fast(st.x - (tm == -INFINITY ? 0.0f : tm));
+            const float tl = across16<false>(st.y * f);
+            if (head < nh) {
+              sh.weight[head][c] = f;
+              if (c == 0) {
+                sh.m[0][head] = tm;
+                sh.l[0][head] = tl;
+              }
+            }
+          }
+          __syncthreads();
 #pragma unroll
-        for (int b = 0; b < kWide; ++b)
-          if (64 * b + lane < n4) mine[64 * b + lane] = sum[b];
-        __syncthreads();
-        for (int i = threadIdx.x; i < n4; i += kThreads) {
-          f32x4 all = reinterpret_cast<const f32x4 *>(sh.tile[0])[i];
+          for (int b = 0; b < kWide; ++b) sum[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int p0 = wave; p0 < parts; p0 += kJoin * kWaves) {
+            if (p0 != wave) load_parts(p0);
 #pragma unroll
-          for (int w = 1; w < kWaves; ++w) all += reinterpret_cast<const f32x4 *>(sh.tile[w])[i];
-          finish(i, i / kQuads, all, sh.m[0][i / kQuads], sh.l[0][i / kQuads]);
+            for (int u = 0; u < kJoin; ++u)
+              if (p0 + u * kWaves < parts)
+#pragma unroll
+                for (int b = 0; b < kWide; ++b)
+                  sum[b] += x[u][b] *
+                            sh.weight[min(64 * b + lane, n4 - 1) / kQuads][p0 + u * kWaves];
+          }
+#pragma unroll
+          for (int b = 0; b < kWide; ++b)
+            if (64 * b + lane < n4) mine[64 * b + lane] = sum[b];
+          __syncthreads();
+          for (int i = threadIdx.x; i < n4; i += kThreads) {
+            const int head = i / kQuads;
+            f32x4 all = reinterpret_cast<const f32x4 *>(sh.tile[0])[i];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) all += reinterpret_cast<const f32x4 *>(sh.tile[w])[i];
+            if (final)
+              finish(i, head, all, sh.m[0][head], sh.l[0][head]);
+            else
+              keep_part(place_of(first), i, head, all, sh.m[0][head], sh.l[0][head]);
+          }
         }
+        if (final) break;
+        final = true;
+        parts = (used + kJoined - 1) / kJoined;
+        step = kJoined;
+        first = 0;
+        ticket = counters + kGridMany;
       }
     }
     pos = g.next;

@@ -305,6 +305,30 @@ def test_attention_of_many_rows(tb, dt, T, kv, gq, dim, longest):  # noqa: F811
                                                + 2 * np.abs(e))).all(), t
 
 
+@pytest.mark.parametrize("kv,gq,dim,lens", [
+    (1, 1, 64, [2048]), (1, 1, 64, [2049]), (1, 3, 128, [4096, 4097]), (1, 1, 64, [32767]),
+    (1, 9, 64, [40000]), (1, 1, 128, [131072]), (2, 2, 64, [33000, 0, 2100, 64, 31]),
+    (1, 2, 256, [9000, 8200]), (1, 1, 64, [70000, 60000] + [1500] * 40),
+])
+def test_attention_of_many_parts(tb, kv, gq, dim, lens):  # noqa: F811
+    """Rows cut into 16, 17, 32 and more parts, up to the most there can be:
+    groups of parts that are full, hold one part or a few."""
+    from tests.test_gpu_decode_step import attend_inputs, check_attention
+    say(f"[run] attention in parts kv={kv} G={gq} D={dim} {lens[:4]}")
+    ps = 64
+    caches, tables, q, ks, vs = attend_inputs(dim, lens, -(-max(lens) // ps), kv, gq, dim, ps,
+                                              "bf16")
+    cache = tb.KvCache(*caches)
+    first = None
+    for _ in range(3):
+        out, lse = tb.bitnet_paged_attention(cache, 1, dev(q), dev(tables),
+                                             dev(np.array(lens, np.int32)), return_lse=True)
+        out, lse = host(out), host(lse)
+        assert first is None or first == out.tobytes() + lse.tobytes()
+        first = out.tobytes() + lse.tobytes()
+    check_attention(out, lse, q, ks, vs, dim ** -0.5, dim, LOST["bf16"])
+
+
 @pytest.mark.parametrize("dt,pages", [("bf16", 150000), ("int8", 280000)])
 def test_cache_past_32_bits(tb, dt, pages):  # noqa: F811
     """Pages whose offsets pass 2^31 elements and 2^32 bytes, in the first layer
