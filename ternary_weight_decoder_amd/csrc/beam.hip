@@ -11,11 +11,12 @@
 // A workgroup takes one chunk of a row, 4096 logits at a time in registers.
 // Each thread keeps its own running maximum and sum of exp.  A 64-bit key (the
 // logit's bits in unsigned order, then the inverted token) makes candidates
-// distinct.  For the chunk's W largest keys every wave finds a bound that W of
-// its lanes' own largest keys reach, bit by bit with ballots; no more than W
-// lanes of any wave reach the largest of the waves' bounds, so the keys that do
-// are few, and are ranked by counting.  Later tiles of the chunk start from the
-// W-th largest so far and mostly end there.
+// distinct.  A wave lists the keys that may be among its W largest: from the
+// first tile those above a bound that W of its lanes' own largest keys reach,
+// found from the top bits down with ballots, and no more than a few lanes do;
+// from later tiles those above that bound, which rises where many would pass it.
+// Nothing in the stream waits for another wave.  The chunk's W largest are then
+// found among the waves' lists with a bound of the same kind, and by counting.
 //
 // The last chunk of a row to finish joins the row's chunks, and the last row of
 // a group the rows, in the same way.  Partial results go through
@@ -123,15 +124,17 @@ struct Entry {
 template <int MAXW>
 struct SelectShared {
   static constexpr int kEntries = MAXW == kMaxWidth ? kMaxWidth * kMaxWidth : kFlat;
-  static constexpr int kKeys = kWaves * MAXW * kPer + MAXW;
-  static constexpr int kWords = 2 * kEntries > kKeys ? 2 * kEntries : kKeys;
-  __attribute__((aligned(16))) u64 cand[kWords];
+  // A wave's list: what one tile can add, and what is left of a list that was cut.
+  static constexpr int kList = 2 * MAXW * kPer;
+  static constexpr int kPerLane = kList / 64;
+  static_assert(MAXW * kPerLane + MAXW * kPer <= kList, "room for a tile's keys");
+  static constexpr int kWords = std::max(2 * kEntries, kWaves * kList);
+  __attribute__((aligned(16))) u64 cand[kWords];   // the waves' lists, then candidates
   u64 best[MAXW];                      // the W largest keys, in order
   double lse[MAXW];
   float from[MAXW];                    // scores of the group's beams, and their flags
   int flag[MAXW];
-  u64 bound[2][kWaves];
-  int above[2][kWaves];
+  u64 bound[kWaves];
   float m[kWaves], s[kWaves];
   uint32_t count, last;
   int winner[MAXW];
@@ -176,40 +179,19 @@ __device__ __forceinline__ u64 wave_bound(u64 key, int W, int most) {
   return ((u64)v << 32) | low;
 }
 
-// sh.best becomes the W largest of sh.best (`have` keys, 0 or W) and of the
-// threads' keys: key(j), j < N <= kPer, 0 for none; mine() is the thread's
-// largest, looked at only where some lane of the wave is `hopeful`: false where
-// the thread holds nothing above sh.best[W - 1].  Every thread calls it, with
-// the workgroup in step; `flip` alternates from call to call.
-template <int N, int MAXW, typename Mine, typename Key>
-__device__ __forceinline__ void select_largest(SelectShared<MAXW> &sh, int W, int have, int flip,
-                                               bool hopeful, Mine mine_of, Key key) {
+// sh.best becomes the W largest, in order, of the threads' keys: key(j), j < N <=
+// kPer, 0 for none; `mine` is the thread's largest.  Every thread calls it, with
+// the workgroup in step, and has its keys in registers.
+template <int N, int MAXW, typename Key>
+__device__ __forceinline__ void select_largest(SelectShared<MAXW> &sh, int W, u64 mine, Key key) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const u64 floor = have ? sh.best[W - 1] : 0;
-  u64 mine = 0, b = 0;
-  int above = 0;
-  if (__any(hopeful)) {
-    mine = mine_of();
-    above = __builtin_popcountll(__ballot(mine > floor));
-    // A wave with few keys above what is there already needs no further bound:
-    // MAXW lanes of a wave fit the list.
-    if (above > (have ? MAXW : W)) b = wave_bound(mine, W, MAXW);
-  }
-  if (lane == 0) {
-    sh.bound[flip][wave] = b;
-    sh.above[flip][wave] = above;
-  }
-  if (tid == 0) sh.count = have;
-  if (tid < have) sh.cand[tid] = sh.best[tid];
+  const u64 b = wave_bound(mine, W, MAXW);
+  if (lane == 0) sh.bound[wave] = b;
+  if (tid == 0) sh.count = 0;
   __syncthreads();
-  u64 bound = floor + 1;
-  int some = 0;
+  u64 bound = 1;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    bound = sh.bound[flip][w] > bound ? sh.bound[flip][w] : bound;
-    some |= sh.above[flip][w];
-  }
-  if (have && some == 0) return;   // the same for every thread
+  for (int w = 0; w < kWaves; ++w) bound = sh.bound[w] > bound ? sh.bound[w] : bound;
   if (mine >= bound)
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -274,12 +256,12 @@ __device__ __forceinline__ void select_group(SelectShared<MAXW> &sh, int W,
   }
   int at = 64;
   const uint32_t b = bound_bits(mine, true, 0, W, W, &at);
-  if (lane == 0) sh.bound[0][wave] = b;
+  if (lane == 0) sh.bound[wave] = b;
   if (tid == 0) sh.count = 0;
   __syncthreads();
   u64 bound = 1;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) bound = sh.bound[0][w] > bound ? sh.bound[0][w] : bound;
+  for (int w = 0; w < kWaves; ++w) bound = sh.bound[w] > bound ? sh.bound[w] : bound;
 #pragma unroll
   for (int j = 0; j < N; ++j)
     if (order[j] >= bound) {
@@ -343,6 +325,35 @@ select_kernel(SelectArgs a, SelectPlan p) {
       }
     };
     load(i0);
+    // The wave's list: every key of its W largest so far, and others, all from
+    // `least`, which W of them reach once there are more than a few.
+    typedef SelectShared<MAXW> Shared;
+    u64 *list = sh.cand + wave * Shared::kList;
+    u64 least = 1;
+    float least_logit = -INFINITY;
+    int listed = 0;
+    auto add = [&](bool in, u64 k) {
+      const u64 m = __ballot(in);
+      if (in) list[listed + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
+                                                      __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0))] = k;
+      listed += __builtin_popcountll(m);
+    };
+    auto cut = [&]() {   // down to the keys of few lanes, W of which are largest
+      u64 k[Shared::kPerLane], mine = 0;
+#pragma unroll
+      for (int j = 0; j < Shared::kPerLane; ++j) {
+        k[j] = lane + 64 * j < listed ? list[lane + 64 * j] : 0;
+        mine = k[j] > mine ? k[j] : mine;
+      }
+      __builtin_amdgcn_wave_barrier();
+      const u64 b = wave_bound(mine, W, MAXW);
+      least = b > least ? b : least;
+      least_logit = logit_of(least);
+      listed = 0;
+#pragma unroll
+      for (int j = 0; j < Shared::kPerLane; ++j) add(k[j] >= least, k[j]);
+      __builtin_amdgcn_wave_barrier();
+    };
     // Sum of exp(x - m), m the running maximum, as exp2(x c - fl(m c)): one fma
     // and one exp2 a logit, and since the join takes the same fl(m c), its
     // rounding cancels.  (Where m c would overflow: exp2((x - m) c).)
@@ -382,16 +393,35 @@ select_kernel(SelectArgs a, SelectPlan p) {
         s = s * shift(m, m_new) + e[0];
         m = m_new;
       }
+      // Keys that may be among the chunk's W largest go to the wave's list.
+      if (!__any(top >= least_logit)) continue;
       auto token = [&](int j) { return at + (j >> 2) * 4 * kThreads + (j & 3); };
-      select_largest<kPer>(
-          sh, W, tile ? W : 0, tile & 1, tile == 0 || top >= logit_of(sh.best[W - 1]),
-          [&]() {   // ties: the first of the thread's, which has the lowest token
-            int where = kPer - 1;
+      int where = kPer - 1;   // ties: the first of the thread's, which has the lowest token
 #pragma unroll
-            for (int j = kPer - 2; j >= 0; --j) where = v[j] == top ? j : where;
-            return at < stop ? key_of(top, (uint32_t)token(where)) : 0;
-          },
-          [&](int j) { return token(j) < stop ? key_of(v[j], (uint32_t)token(j)) : 0; });
+      for (int j = kPer - 2; j >= 0; --j) where = v[j] == top ? j : where;
+      const u64 mine = at < stop ? key_of(top, (uint32_t)token(where)) : 0;
+      const int above = __builtin_popcountll(__ballot(mine >= least));
+      if (above == 0) continue;
+      if (above > MAXW) {
+        least = wave_bound(mine, W, MAXW);
+        least_logit = logit_of(least);
+      }
+      if (listed + MAXW * kPer > Shared::kList) cut();
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (__any(v[j] >= least_logit)) {
+          const u64 k = token(j) < stop ? key_of(v[j], (uint32_t)token(j)) : 0;
+          add(k >= least, k);
+        }
+    }
+    {
+      u64 k[Shared::kPerLane], mine = 0;
+#pragma unroll
+      for (int j = 0; j < Shared::kPerLane; ++j) {
+        k[j] = lane + 64 * j < listed ? list[lane + 64 * j] : 0;
+        mine = k[j] > mine ? k[j] : mine;
+      }
+      select_largest<Shared::kPerLane>(sh, W, mine, [&](int j) { return k[j]; });
     }
     // The chunk's maximum and sum.
     const float top = across16<true>(across4(m));
@@ -502,8 +532,7 @@ select_kernel(SelectArgs a, SelectPlan p) {
         const double v = log_sum(e, sum);
         if (lane == 0) sh.lse[0] = v;
       }
-      select_largest<kJoinPer>(sh, W, 0, 0, true, [&]() { return mine; },
-                               [&](int j) { return k[j]; });
+      select_largest<kJoinPer>(sh, W, mine, [&](int j) { return k[j]; });
       if (tid < W) {
         const u64 key = sh.best[tid];
         const double t = base + ((double)logit_of(key) - sh.lse[0]);
