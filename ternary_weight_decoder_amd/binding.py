@@ -168,15 +168,15 @@ def _check(status: int, fn: str) -> None:
         raise BitnetError(status, fn)
 
 
-def _ptr(t):
-    return None if t is None else _p(t.data_ptr())
+def _ptr(t):   # (an int: every function's argtypes are declared)
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
     if stream is not None:
-        return _p(stream.cuda_stream)
+        return stream.cuda_stream
     # (torch.cuda.current_stream() builds an object: 2.7 us a call against 0.4.)
-    return _p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dev(t: torch.Tensor, dtype, name: str) -> None:
