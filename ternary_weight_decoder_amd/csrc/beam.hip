@@ -22,6 +22,11 @@
 // a group the rows, in the same way.  Partial results go through
 // device-coherent accesses, and the counters that tell the last are left at
 // zero.
+//
+// Measured (151,936 logits a row, inputs rotating, a launch in a graph): 32
+// groups of 8 beams 39.6 us (139.5 MB, reads within 0.3% of it; waves wait 47% of
+// their time; with a barrier and a ranking in every tile 44.2), one group of 4
+// beams 11.8, one greedy row 8.5, of which a launch is 1.8.
 #include <algorithm>
 
 #include "bitnet_device.hpp"
@@ -41,9 +46,9 @@ constexpr int kMaxChunks = 64;                       // of a row
 constexpr int kJoinPer = kMaxChunks * kMaxWidth / kThreads;
 constexpr int kCounters = kMaxRows;                  // of rows; as many of groups behind them
 constexpr int kHeaderBytes = 2 * 4 * kCounters;
-// Workgroups before a workgroup takes more than one tile: four a compute unit, as
-// many as its registers hold.  256 rows of 151,936 logits: 44 us, as with 1536;
-// 2048 take 49, 512 take 58.  One group of 32 such rows: 40 us, 55 with 1536.
+// Workgroups before a workgroup takes more than one tile: four a compute unit.
+// 256 rows of 151,936 logits: 39.6 us; 39.9 with 768, 44.4 with 1536, 46.8 with
+// 2048.  One group of 32 such rows: 39 us, 55 with 1536 or more.
 constexpr int kTargetGroups = 1024;
 constexpr int kSimdWaves = 4;
 
