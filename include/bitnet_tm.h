@@ -598,7 +598,8 @@ bitnet_status bitnet_kv_map(const bitnet_kv_pool *pool, int64_t T, const int32_t
  *   [T][q_heads*head_dim] takes the rotated queries.  q (then q_out too) may
  *   be NULL to rotate only k; without cos and sin (both NULL) nothing is
  *   rotated, positions may be NULL and q and q_out have to be.
- *   The stored value is the rounded (half to even) or quantized fp32 row.
+ *   The stored value is the rounded (half to even) or quantized fp32 row; of an
+ *   8-bit row with infinities or NaN the codes and the scale are unspecified.
  *   A token whose slot is outside [0, pages*page_size), or whose position is
  *   outside [0, max_pos) where it is used, is skipped: nothing of it is
  *   written, q_out included.  Slots of one call must differ from each other.
@@ -635,7 +636,11 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, int32_t layer, int6
  *   below 2^23, T * kv_heads (times 2, 3, 4 for more than 16, 32, 48 query
  *   heads per kv head) and max_pages below 2^31, max_len below 2^30; q and out
  *   16-byte aligned, q_stride a multiple of 4 and below 2^31.
- *   T == 0 launches nothing.  out, lse and the inputs must not overlap.
+ *   q and the tokens in use are finite, scale is finite (else BITNET_ERR_SHAPE),
+ *   and scale * q stays below 2^125; rows that break this give unspecified
+ *   outputs of their own and leave the others alone.
+ *   T == 0 launches nothing.  out, lse and workspace must overlap neither each
+ *   other, nor the inputs, nor the layer.
  *   workspace: bitnet_paged_attention_workspace_bytes(...) bytes, 256-byte
  *   aligned, ZERO-FILLED before its first use and written by nothing else
  *   (its first 16 KB hold counters that every call leaves at zero; calls of
@@ -693,8 +698,8 @@ bitnet_status bitnet_beam_select(int64_t B, int64_t W, int64_t V, const float *l
  *   that has no child, and the tokens in use are copied into it, in every
  *   layer.  (There are as many of the one as of the other.)  So the last pages
  *   of a group's rows, as passed in, must differ from each other.
- *   tables_in, tables_out int32 [B*W][max_pages], apart from each other;
- *   entries behind the length are the row's own from tables_in.  A parent
+ *   tables_in, tables_out int32 [B*W][max_pages], apart from each other and
+ *   tables_out from the cache; entries behind the length are the row's own from tables_in.  A parent
  *   outside the group counts as the row itself; lengths are clamped to
  *   [0, max_pages * page_size]; a copy from or to a page outside [0, pages)
  *   is left out.  B*W <= 4096, 1 <= W <= 32.  One launch.

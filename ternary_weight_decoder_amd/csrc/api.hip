@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <utility>
@@ -817,6 +818,27 @@ static bool overlaps_any(const Range *r, int nout, int n) {
   return false;
 }
 
+// The cache's arrays of `layers` layers from `layer` on, from the first element to
+// the last (other things may lie between its rows: only outputs are held against it).
+static bool overlaps_cache(const bitnet_kv_cache *c, int32_t layer, int32_t layers,
+                           const Range *r, int nout) {
+  const bool i8 = c->dtype == BITNET_KV_INT8;
+  const int64_t es = i8 ? 1 : 2, ls = c->layers > 1 ? c->layer_stride : 0;
+  const __int128 last = (__int128)(layers - 1) * ls + (__int128)(c->pages - 1) * c->page_stride +
+                        (__int128)(c->kv_heads - 1) * c->head_stride +
+                        (__int128)(c->page_size - 1) * c->token_stride + c->head_dim;
+  const int64_t bytes = (int64_t)std::min<__int128>(last * es, (__int128)1 << 62);
+  const int64_t scales = (int64_t)c->pages * c->kv_heads * c->page_size;
+  const Range a[] = {{static_cast<uint8_t *>(c->k) + layer * ls * es, bytes},
+                     {static_cast<uint8_t *>(c->v) + layer * ls * es, bytes},
+                     {i8 ? c->k_scale + layer * scales : nullptr, layers * scales * 4},
+                     {i8 ? c->v_scale + layer * scales : nullptr, layers * scales * 4}};
+  for (int i = 0; i < nout; ++i)
+    for (const Range &x : a)
+      if (overlap(r[i], x)) return true;
+  return false;
+}
+
 static bool power_of_two(int64_t v) { return v >= 1 && (v & (v - 1)) == 0; }
 
 static int shift_of(int64_t v) {
@@ -951,7 +973,7 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, int32_t layer, int6
                        {positions, T * 4},
                        {cos, max_pos * D * 2},
                        {sin, max_pos * D * 2}};
-    if (overlaps_any(r, 1, 8)) return BITNET_ERR_ALIAS;
+    if (overlaps_any(r, 1, 8) || overlaps_cache(cache, layer, 1, r, 1)) return BITNET_ERR_ALIAS;
   }
   st = device_check();
   if (st != BITNET_OK) return st;
@@ -1003,7 +1025,8 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
   const int64_t D = cache->head_dim, qd = q_heads * D;
   if (!attend_shape_ok(T, q_heads, cache->kv_heads, D, max_len) || q_stride < qd ||
       q_stride >= kLimit || table_rows < 1 || table_rows >= kMaxTokens || max_pages < 1 ||
-      max_pages >= kLimit || max_len > max_pages * cache->page_size || (!rows && T > table_rows))
+      max_pages >= kLimit || max_len > max_pages * cache->page_size ||
+      (!rows && T > table_rows) || !std::isfinite(scale))
     return BITNET_ERR_SHAPE;
   if (q_stride % 4 || !aligned(q, 16) || !aligned(out, 16) || !aligned(tables, 4) ||
       !aligned(lens, 4) || (rows && !aligned(rows, 4)) || (lse && !aligned(lse, 4)))
@@ -1018,7 +1041,7 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
                      {tables, table_rows * max_pages * 4},
                      {rows, T * 4},
                      {lens, T * 4}};
-  if (overlaps_any(r, 3, 7)) return BITNET_ERR_ALIAS;
+  if (overlaps_any(r, 3, 7) || overlaps_cache(cache, layer, 1, r, 3)) return BITNET_ERR_ALIAS;
   st = device_check();
   if (st != BITNET_OK) return st;
   AttendArgs a;
@@ -1099,8 +1122,8 @@ bitnet_status bitnet_beam_reorder(const bitnet_kv_cache *cache, int64_t B, int64
   bitnet_status st = check_cache(cache, 0);
   if (st != BITNET_OK) return st;
   if (!parents || !lens || !tables_in || !tables_out) return BITNET_ERR_NULL;
-  if (!beams_ok(B, W) || max_pages < 1 || max_pages * cache->page_size >= kLimit ||
-      max_pages >= kLimit)
+  if (!beams_ok(B, W) || max_pages < 1 || max_pages >= kLimit ||
+      max_pages * cache->page_size >= kLimit)
     return BITNET_ERR_SHAPE;
   if (!aligned(parents, 4) || !aligned(lens, 4) || !aligned(tables_in, 4) ||
       !aligned(tables_out, 4))
@@ -1108,7 +1131,8 @@ bitnet_status bitnet_beam_reorder(const bitnet_kv_cache *cache, int64_t B, int64
   const int64_t n = B * W * 4;
   const Range r[] = {{tables_out, n * max_pages}, {tables_in, n * max_pages}, {parents, n},
                      {lens, n}};
-  if (overlaps_any(r, 1, 4)) return BITNET_ERR_ALIAS;
+  if (overlaps_any(r, 1, 4) || overlaps_cache(cache, 0, cache->layers, r, 1))
+    return BITNET_ERR_ALIAS;
   st = device_check();
   if (st != BITNET_OK) return st;
   ReorderArgs a;

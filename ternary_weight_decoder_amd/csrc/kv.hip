@@ -275,8 +275,8 @@ constexpr int64_t kMapTokensHere = 4096;
 // reduction over head_dim / 8 adjacent lanes.  Bound by memory, short calls by the
 // launch: 1800 tokens of 12 + 2 * 2 heads of 128 channels 8.8 us for 28.6 MB (9.3
 // with the activations asked for after the slot), 16 tokens 2.5; 4096 tokens of
-// 32 + 2 * 8 heads of 256 channels 72 us, 5.2 TB/s.  Rotations in fp64 cost
-// nothing beside the stream.
+// 32 + 2 * 8 heads of 256 channels 72 us, 5.2 TB/s: the stream hides the fp64
+// rotations.
 // ---------------------------------------------------------------------------
 
 template <int DT> struct KvElem;

@@ -235,3 +235,48 @@ def test_reorder_definition_by_hand():
     assert nk[0, :, 0, 0, 0].tolist() == [0, 1, 2, 3, 5, 5, 6, 6]   # 2 tokens copied ...
     assert nk[0, :, 0, 2, 0].tolist() == [0, 1, 2, 3, 4, 5, 6, 7]   # ... and no more
     assert nv[0, 4, 0, :, 0].tolist() == [5, 5, 4, 4]
+
+
+def test_outputs_inside_the_cache_are_refused(L):
+    """The layer's arrays from their first to their last element; ALIAS is decided
+    before the device is looked at, so where there is none a call that passes this
+    check gives something else."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("calls that pass the checks would run on made-up addresses")
+    c = dict(k=A + 8 * GB, v=A + 16 * GB)
+    last = ((63 << 14) + (1 << 13) + 63 * 128 + 127) * 2      # of a layer, bytes
+    lay = 1 << 21
+    for base in (8, 16):
+        for layer in (0, 1):
+            at = A + base * GB + layer * lay
+            assert append(L, cache(**c), layer, qo=at + 1024) == ALIAS
+            assert append(L, cache(**c), layer, qo=at + last - 14) == ALIAS
+            assert append(L, cache(**c), layer, qo=at - 16) == ALIAS
+            for kw in (dict(out=at + 4096), dict(lse=at + last - 2), dict(ws=at + 512)):
+                assert attend(L, cache(**c), layer, **kw) == ALIAS, kw
+            assert reorder(L, cache(**c), to=at + last - 2) == ALIAS
+        # the other layer is not this call's
+        assert append(L, cache(**c), 0, qo=A + base * GB + lay) != ALIAS
+    assert append(L, cache(**c), 1, qo=A + 4 * GB) != ALIAS
+    s = dict(c, dtype=2, k_scale=A + 24 * GB, v_scale=A + 25 * GB)
+    per = 64 * 2 * 64 * 4
+    for base in (24, 25):
+        assert attend(L, cache(**s), 1, out=A + base * GB + 2 * per - 16) == ALIAS
+        assert attend(L, cache(**s), 0, out=A + base * GB + per) != ALIAS
+        assert reorder(L, cache(**s), to=A + base * GB + 2 * per - 4) == ALIAS
+
+
+def test_extents_of_huge_strides_do_not_wrap(L):
+    c = cache(k=A + 8 * GB, v=A + 16 * GB, page_stride=(1 << 31) - 8, pages=(1 << 24) - 1,
+              page_size=128, layers=1024, layer_stride=(1 << 40) - 8)
+    assert append(L, c, 0, qo=A + 64 * GB) == ALIAS
+    assert reorder(L, c, to=A + 64 * GB) == ALIAS
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_attention_scale_is_finite(L, scale):
+    c = cache(k=A + 8 * GB, v=A + 16 * GB)
+    ws = L.bitnet_paged_attention_workspace_bytes(4, 12, 2, 128, 512)
+    assert L.bitnet_paged_attention(ctypes.byref(c), 0, 4, 12, A, 1536, A, 4, 8, None, A, 512, scale,
+                                    A + GB, None, A + 2 * GB, ws, None) == SHAPE
