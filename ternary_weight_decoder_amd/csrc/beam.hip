@@ -129,9 +129,8 @@ struct Entry {
   u64 key;
 };
 
-// By the greatest width a kernel serves: room for the keys that reach a bound (as
-// many lanes of a wave, kPer keys each, and those that were there), and for a
-// group's candidates, which may all tie.
+// By the greatest width a kernel serves: room for the waves' lists (all of which may
+// reach the bound of their join) and for a group's candidates (which may all tie).
 template <int MAXW>
 struct SelectShared {
   static constexpr int kEntries = MAXW == kMaxWidth ? kMaxWidth * kMaxWidth : kFlat;
@@ -177,6 +176,7 @@ __device__ __forceinline__ uint32_t bound_bits(uint32_t key, bool in, int above,
     }
   return v;
 }
+// Maximum over the wave, in every lane.
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
