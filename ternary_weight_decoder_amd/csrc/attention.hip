@@ -514,10 +514,8 @@ attend_kernel(AttendArgs a, AttendGrid g0) {
         off[i] = (uint64_t)page * page_bytes + (uint64_t)tok * tok_bytes;
         if constexpr (kI8) {
           const uint32_t at = ((page * (uint32_t)a.c.kv_heads + kvh) << a.c.page_shift) + tok;
-          const float ks = ld_global<float>(a.c.k_scale + at);
-          const float vs = ld_global<float>(a.c.v_scale + at);
-          ksc[i] = ok ? ks : 0.0f;
-          vsc[i] = ok ? vs : 0.0f;
+          ksc[i] = ld_global<float>(a.c.k_scale + at);   // (looked at with the rows)
+          vsc[i] = ld_global<float>(a.c.v_scale + at);
         }
         m[i] = (uint32_t)__ballot(ok) & 0xffffu;
       }
@@ -602,6 +600,12 @@ attend_kernel(AttendArgs a, AttendGrid g0) {
       // to the power of two above the largest so far.
       float ks[8], vs[8], vkeep = 1.0f;
       if constexpr (kI8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bool ok = (mask >> (c + 16 * i)) & 1;
+          ksc[i] = ok ? ksc[i] : 0.0f;
+          vsc[i] = ok ? vsc[i] : 0.0f;
+        }
         const float v_new = fmaxf(vmax, pow2_above(across16<true>(fmaxf(vsc[0], vsc[1]))));
         const float inv = pow2_inverse(v_new);
         vkeep = vmax * inv;
