@@ -38,7 +38,7 @@
 // Measured (2 key/value heads of 128 channels, 12 query heads, inputs rotating,
 // a launch in a graph): 64 bf16 rows of 1800-32,768 tokens 184-187 us, 6.1 TB/s,
 // reads within 0.5% of the cache's bytes, waves waiting 26% of their time; one
-// fp16 row of 32,767 tokens 17.3 us; 16 int8 rows of 225-1801 tokens 12.2; one
+// fp16 row of 32,767 tokens 17.3 us; 16 int8 rows of 225-1801 tokens 11.4; one
 // row of 257 tokens 9.3, a chain of fetches that a launch (1.8 us) begins.
 #include <algorithm>
 
@@ -514,7 +514,8 @@ attend_kernel(AttendArgs a, AttendGrid g0) {
         off[i] = (uint64_t)page * page_bytes + (uint64_t)tok * tok_bytes;
         if constexpr (kI8) {
           const uint32_t at = ((page * (uint32_t)a.c.kv_heads + kvh) << a.c.page_shift) + tok;
-          ksc[i] = ld_global<float>(a.c.k_scale + at);   // (looked at with the rows)
+          // (Looked at only with the rows: a select here waits for them, 10% of the time.)
+          ksc[i] = ld_global<float>(a.c.k_scale + at);
           vsc[i] = ld_global<float>(a.c.v_scale + at);
         }
         m[i] = (uint32_t)__ballot(ok) & 0xffffu;
