@@ -747,7 +747,7 @@ def bitnet_kv_map_into(pool: KvPool, T, new_lens, state_in, state_out, starts, s
 
 def _rows_stride(t, width):
     """Elements between the rows of a [T, width] tensor with contiguous rows."""
-    return t.stride(0) if t.shape[0] > 1 else max(width, 4)
+    return t.stride(0) if t.size(0) > 1 else max(width, 4)
 
 
 def bitnet_kv_append_into(cache: KvCache, layer, T, q_heads, k, v, slots, positions=None, cos=None,
@@ -755,7 +755,7 @@ def bitnet_kv_append_into(cache: KvCache, layer, T, q_heads, k, v, slots, positi
     w = cache.kv_heads * cache.head_dim
     _check(lib().bitnet_kv_append(cache.ref, layer, T, q_heads, _ptr(k), _rows_stride(k, w),
                                   _ptr(v), _rows_stride(v, w), _ptr(slots), _ptr(positions),
-                                  _ptr(cos), _ptr(sin), 0 if cos is None else cos.shape[0],
+                                  _ptr(cos), _ptr(sin), 0 if cos is None else cos.size(0),
                                   _ptr(q),
                                   0 if q is None else _rows_stride(q, q_heads * cache.head_dim),
                                   _ptr(q_out), _stream(stream)),
@@ -773,7 +773,7 @@ def bitnet_paged_attention_into(cache: KvCache, layer, T, q_heads, q, tables, le
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().bitnet_paged_attention(cache.ref, layer, T, q_heads, _ptr(q),
                                         _rows_stride(q, q_heads * cache.head_dim), _ptr(tables),
-                                        tables.shape[0], tables.shape[1], _ptr(rows), _ptr(lens),
+                                        tables.size(0), tables.size(1), _ptr(rows), _ptr(lens),
                                         max_len, scale, _ptr(out), _ptr(lse), _ptr(workspace),
                                         ws_bytes, _stream(stream)),
            "bitnet_paged_attention")
@@ -796,7 +796,7 @@ def bitnet_beam_select_into(B, W, V, logits, scores_in, finished_in, eos, scores
 def bitnet_beam_reorder_into(cache: KvCache, B, W, parents, lens, tables_in, tables_out,
                              stream=None) -> None:
     _check(lib().bitnet_beam_reorder(cache.ref, B, W, _ptr(parents), _ptr(lens), _ptr(tables_in),
-                                     _ptr(tables_out), tables_in.shape[1], _stream(stream)),
+                                     _ptr(tables_out), tables_in.size(1), _stream(stream)),
            "bitnet_beam_reorder")
 
 
