@@ -90,6 +90,9 @@ constexpr int kLine = 8;           // tiles of a stretch that is shared by items
 constexpr int kJoined = 16;
 constexpr int kMaxParts = kJoined * kJoined;   // stretches that one item may lie in
 constexpr int kLineRows = 1024;    // rows whose lengths a workgroup sums up itself
+// A grid's first axis holds fewer than 2^32 threads: a workgroup per item takes
+// as many rows of workgroups as it needs.
+constexpr int64_t kGridAxis = (int64_t)1 << 23;
 constexpr int kHeaderBytes = 16384;
 static_assert(8 * kGridMany <= kHeaderBytes, "two counters per stretch");
 
@@ -299,7 +302,8 @@ struct Segment {
 // heads, items per row.
 struct AttendGrid {
   int64_t stats_off;
-  int32_t line, per, groups, row_items, grid;
+  int32_t line, per, groups, row_items;
+  int32_t grid;   // workgroups of the first axis
 };
 
 // FEW: up to 64 rows, whose lengths every wave holds a lane each.  (A kernel of
@@ -339,7 +343,8 @@ attend_kernel(AttendArgs a, AttendGrid g0) {
 
   // This workgroup's stretch [pos, stop) of the line.
   int my_row = 0, my_len = 0, my_start = 0;
-  int pos = 0, stop = 1, stretch = 1;
+  const uint32_t item = blockIdx.y * (uint32_t)g0.grid + blockIdx.x;   // without a line
+  int pos = 0, stop = item < (uint32_t)(a.T * row_items) ? 1 : 0, stretch = 1;
   bool apart = false;                  // every item starts a stretch
   // (Exact: the quotients are below 2^13, so half a unit outweighs the error of
   // the reciprocal.)
@@ -436,8 +441,8 @@ attend_kernel(AttendArgs a, AttendGrid g0) {
   auto locate = [&]() {
     Segment g;
     if (!line) {   // a workgroup per item
-      g.t = blockIdx.x / row_items;
-      g.in_row = blockIdx.x - g.t * row_items;
+      g.t = item / (uint32_t)row_items;
+      g.in_row = item - (uint32_t)(g.t * row_items);
       g.table_row = table_row(g.t);
       g.len = length(g.t, g.table_row);
       g.tiles = g.end = tiles_of(g.len);
@@ -905,11 +910,11 @@ attend_kernel(AttendArgs a, AttendGrid g0) {
 }
 
 template <int DT, int D, bool FOLD>
-void attend_rows(const AttendArgs &a, const AttendGrid &g, hipStream_t stream) {
+void attend_rows(const AttendArgs &a, const AttendGrid &g, const dim3 &grid, hipStream_t stream) {
   if (a.T <= 64 && g.line)
-    attend_kernel<DT, D, FOLD, true><<<g.grid, kThreads, 0, stream>>>(a, g);
+    attend_kernel<DT, D, FOLD, true><<<grid, kThreads, 0, stream>>>(a, g);
   else
-    attend_kernel<DT, D, FOLD, false><<<g.grid, kThreads, 0, stream>>>(a, g);
+    attend_kernel<DT, D, FOLD, false><<<grid, kThreads, 0, stream>>>(a, g);
 }
 
 template <int DT, bool FOLD>
@@ -921,13 +926,15 @@ void attend_dim(const AttendArgs &a, int D, hipStream_t stream) {
   g.per = a.q_heads / a.c.kv_heads;
   g.groups = (g.per + kHeads - 1) / kHeads;
   g.row_items = a.c.kv_heads * g.groups;
-  g.grid = (int32_t)p.groups;
+  const int64_t axes = (p.groups + kGridAxis - 1) / kGridAxis;
+  g.grid = (int32_t)((p.groups + axes - 1) / axes);
+  const dim3 grid((unsigned)g.grid, (unsigned)axes);
   if (D == 64)
-    attend_rows<DT, 64, FOLD>(a, g, stream);
+    attend_rows<DT, 64, FOLD>(a, g, grid, stream);
   else if (D == 128)
-    attend_rows<DT, 128, FOLD>(a, g, stream);
+    attend_rows<DT, 128, FOLD>(a, g, grid, stream);
   else
-    attend_rows<DT, 256, FOLD>(a, g, stream);
+    attend_rows<DT, 256, FOLD>(a, g, grid, stream);
 }
 
 template <int DT>
