@@ -604,7 +604,8 @@ bitnet_status bitnet_kv_map(const bitnet_kv_pool *pool, int64_t T, const int32_t
  *   outside [0, max_pos) where it is used, is skipped: nothing of it is
  *   written, q_out included.  Slots of one call must differ from each other.
  *   T == 0 launches nothing.  q_out == q is allowed for contiguous rows; other
- *   overlaps are BITNET_ERR_ALIAS.  q, k, v, q_out, cos and sin 16-byte
+ *   overlaps of q_out, and inputs inside the layer's elements or scales, are
+ *   BITNET_ERR_ALIAS.  q, k, v, q_out, cos and sin 16-byte
  *   aligned, row strides multiples of 4 and below 2^31 elements; T,
  *   q_heads*head_dim and max_pos below 2^23.  One launch.
  */
@@ -698,8 +699,10 @@ bitnet_status bitnet_beam_select(int64_t B, int64_t W, int64_t V, const float *l
  *   that has no child, and the tokens in use are copied into it, in every
  *   layer.  (There are as many of the one as of the other.)  So the last pages
  *   of a group's rows, as passed in, must differ from each other.
- *   tables_in, tables_out int32 [B*W][max_pages], apart from each other and
- *   tables_out from the cache; entries behind the length are the row's own from tables_in.  A parent
+ *   tables_in, tables_out int32 [B*W][max_pages]; tables_out lies apart from the
+ *   other arrays, and parents, lens and tables_in outside the cache's elements
+ *   and scales (else BITNET_ERR_ALIAS).  Entries behind the length are the
+ *   row's own from tables_in.  A parent
  *   outside the group counts as the row itself; lengths are clamped to
  *   [0, max_pages * page_size]; a copy from or to a page outside [0, pages)
  *   is left out.  B*W <= 4096, 1 <= W <= 32.  One launch.

@@ -818,10 +818,36 @@ static bool overlaps_any(const Range *r, int nout, int n) {
   return false;
 }
 
-// The cache's arrays of `layers` layers from `layer` on, from the first element to
-// the last (other things may lie between its rows: only outputs are held against it).
+// One axis of the cache's rows: how many, and the bytes from one to the next.
+struct Axis {
+  int64_t n;
+  __int128 stride;
+};
+
+// Whether bytes [lo, hi) meet the rows of `row` bytes along the n axes, which go from
+// the widest stride down.  (Axes that run into each other count with what lies
+// between their rows.)
+static bool meets_rows(const Axis *x, int n, int64_t row, __int128 lo, __int128 hi) {
+  __int128 span = row;   // of one step of the first axis
+  for (int i = 1; i < n; ++i) span += (x[i].n - 1) * x[i].stride;
+  if (n == 0 || x[0].stride < span)
+    return hi > 0 && lo < span + (n ? (x[0].n - 1) * x[0].stride : 0);
+  if (hi <= 0) return false;
+  const __int128 s = x[0].stride;
+  const __int128 first = lo < span ? 0 : (lo - span) / s + 1;
+  const __int128 last = std::min<__int128>(x[0].n - 1, (hi - 1) / s);
+  if (last - first >= 2) return true;   // those between the two lie inside
+  for (__int128 i = first; i <= last; ++i)
+    if (meets_rows(x + 1, n - 1, row, lo - i * s, hi - i * s)) return true;
+  return false;
+}
+
+// Whether one of n arrays, of which the call writes the first `nout`, meets the
+// cache's arrays of `layers` layers from `layer` on.  Outputs are held against all
+// that lies between the first element and the last, inputs against the elements:
+// they may lie between the rows of a strided cache.
 static bool overlaps_cache(const bitnet_kv_cache *c, int32_t layer, int32_t layers,
-                           const Range *r, int nout) {
+                           const Range *r, int nout, int n) {
   const bool i8 = c->dtype == BITNET_KV_INT8;
   const int64_t es = i8 ? 1 : 2, ls = c->layers > 1 ? c->layer_stride : 0;
   const __int128 last = (__int128)(layers - 1) * ls + (__int128)(c->pages - 1) * c->page_stride +
@@ -833,9 +859,22 @@ static bool overlaps_cache(const bitnet_kv_cache *c, int32_t layer, int32_t laye
                      {static_cast<uint8_t *>(c->v) + layer * ls * es, bytes},
                      {i8 ? c->k_scale + layer * scales : nullptr, layers * scales * 4},
                      {i8 ? c->v_scale + layer * scales : nullptr, layers * scales * 4}};
-  for (int i = 0; i < nout; ++i)
-    for (const Range &x : a)
-      if (overlap(r[i], x)) return true;
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < 4; ++j) {
+      if (!overlap(r[i], a[j])) continue;
+      if (i < nout || j >= 2) return true;
+      Axis x[4];
+      int axes = 0;
+      const Axis all[] = {{layers, ls * es},
+                          {c->pages, c->page_stride * es},
+                          {c->kv_heads, c->head_stride * es},
+                          {c->page_size, c->token_stride * es}};
+      for (const Axis &y : all)
+        if (y.n > 1) x[axes++] = y;
+      std::sort(x, x + axes, [](const Axis &p, const Axis &q) { return p.stride > q.stride; });
+      const __int128 lo = (__int128)(uintptr_t)r[i].p - (__int128)(uintptr_t)a[j].p;
+      if (meets_rows(x, axes, c->head_dim * es, lo, lo + r[i].bytes)) return true;
+    }
   return false;
 }
 
@@ -963,18 +1002,16 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, int32_t layer, int6
       (rotate && (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(positions, 4))) ||
       (q && (!aligned(q, 16) || !aligned(q_out, 16))))
     return BITNET_ERR_ALIGN;
-  if (q) {
-    const bool in_place = q_out == q && q_stride == qd;
-    const Range r[] = {{q_out, T * qd * 4},
-                       {in_place ? nullptr : q, ((T - 1) * q_stride + qd) * 4},
-                       {k, ((T - 1) * k_stride + kd) * 4},
-                       {v, ((T - 1) * v_stride + kd) * 4},
-                       {slots, T * 4},
-                       {positions, T * 4},
-                       {cos, max_pos * D * 2},
-                       {sin, max_pos * D * 2}};
-    if (overlaps_any(r, 1, 8) || overlaps_cache(cache, layer, 1, r, 1)) return BITNET_ERR_ALIAS;
-  }
+  const bool in_place = q_out == q && q_stride == qd;
+  const Range r[] = {{q_out, T * qd * 4},
+                     {in_place ? nullptr : q, q ? ((T - 1) * q_stride + qd) * 4 : 0},
+                     {k, ((T - 1) * k_stride + kd) * 4},
+                     {v, ((T - 1) * v_stride + kd) * 4},
+                     {slots, T * 4},
+                     {rotate ? positions : nullptr, T * 4},
+                     {cos, rotate ? max_pos * D * 2 : 0},
+                     {sin, rotate ? max_pos * D * 2 : 0}};
+  if (overlaps_any(r, 1, 8) || overlaps_cache(cache, layer, 1, r, 1, 8)) return BITNET_ERR_ALIAS;
   st = device_check();
   if (st != BITNET_OK) return st;
   KvAppendArgs a;
@@ -1041,7 +1078,7 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
                      {tables, table_rows * max_pages * 4},
                      {rows, T * 4},
                      {lens, T * 4}};
-  if (overlaps_any(r, 3, 7) || overlaps_cache(cache, layer, 1, r, 3)) return BITNET_ERR_ALIAS;
+  if (overlaps_any(r, 3, 7) || overlaps_cache(cache, layer, 1, r, 3, 3)) return BITNET_ERR_ALIAS;
   st = device_check();
   if (st != BITNET_OK) return st;
   AttendArgs a;
@@ -1131,7 +1168,7 @@ bitnet_status bitnet_beam_reorder(const bitnet_kv_cache *cache, int64_t B, int64
   const int64_t n = B * W * 4;
   const Range r[] = {{tables_out, n * max_pages}, {tables_in, n * max_pages}, {parents, n},
                      {lens, n}};
-  if (overlaps_any(r, 1, 4) || overlaps_cache(cache, 0, cache->layers, r, 1))
+  if (overlaps_any(r, 1, 4) || overlaps_cache(cache, 0, cache->layers, r, 1, 4))
     return BITNET_ERR_ALIAS;
   st = device_check();
   if (st != BITNET_OK) return st;
