@@ -57,3 +57,87 @@ def test_attention_of_more_items_than_a_grid_axis_holds(tb):  # noqa: F811
             bound = U * ((D + 16) * big + n + 64 + 2 * e.abs())
             assert torch.equal(got == -float("inf"), none)
             assert ((got - e).abs() <= bound)[~none].all().item(), (t0, h)
+
+
+def stretches(lens, kv, G, D, max_len):
+    """How the kernel cuts the tiles of these rows: "items" (a workgroup each),
+    "apart" (every item starts a stretch) or "shared" (stretches hold parts of
+    several items), and the tiles of a stretch.  The rule that the kernel's comments
+    give, for choosing inputs that reach each case."""
+    T, row_items = len(lens), kv * (-(-G // 16))
+    items, tiles = T * row_items, -(-max_len // 32)
+    if T > 1024 or items * tiles >= 1 << 30:
+        return "items", 0
+    grid = min(2048 if 2 * items > 512 else 256 if D == 256 else 512, items * (tiles // 4 + 2))
+    per = [-(-int(n) // 32) for n in lens]
+    raw, most = sum(per) * row_items, max(per)
+    rounds = lambda n: -(-n // 4) * 4
+    least = most // 254 + 1
+    stretch = rounds(max(-(-raw // 256), 12 if most <= 12 else 1, least))
+    if stretch <= 16 and items * stretch + raw <= grid * stretch:
+        return "apart", stretch
+    return "shared", rounds(max(-(-raw // grid), 8, least))
+
+
+def check_rows(out, lse, q, rows, lens, ks, vs, scale, D, lost):
+    """Every output against 64-bit arithmetic, a key/value head's queries at once."""
+    T, kv = len(rows), ks[0].shape[0]
+    H = q.shape[1] // D
+    out, q = out.reshape(T, kv, -1, D), q.reshape(T, kv, -1, D).astype(np.float64)
+    lse = lse.reshape(T, kv, -1)
+    kabs, vabs = [np.abs(k) for k in ks], [np.abs(v) for v in vs]
+    for t in range(T):
+        n = int(lens[t])
+        if n == 0:
+            assert (out[t] == 0).all() and (lse[t] == -np.inf).all(), t
+            continue
+        for h in range(kv):
+            k, v = ks[rows[t]][h, :n], vs[rows[t]][h, :n]
+            s = scale * (q[t, h] @ k.T)
+            m = s.max(1, keepdims=True)
+            p = np.exp(s - m)
+            total = p.sum(1, keepdims=True)
+            e = (m + np.log(total))[:, 0]
+            p /= total
+            size = (scale * (np.abs(q[t, h]) @ kabs[rows[t]][h, :n].T)).max(1)
+            tol = U * (2 * (D + 16) * size + 2 * n + 64)[:, None] * (p @ vabs[rows[t]][h, :n])
+            tol += n * lost * vabs[rows[t]][h, :n].max()
+            err = np.abs(out[t, h] - p @ v)
+            assert (err <= tol).all(), (t, h, n, float((err / tol).max()))
+            bound = U * ((D + 16) * size + n + 64 + 2 * np.abs(e))
+            assert (np.abs(lse[t, h] - e) <= bound).all(), (t, h, n)
+    assert H == kv * out.shape[2]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "int8"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [5, 17])
+@pytest.mark.parametrize("cut,T", [("shared", 40), ("shared", 150), ("apart", 70), ("items", 1030)])
+def test_attention_in_every_variant(tb, dt, D, G, cut, T):  # noqa: F811
+    """Each type, head size and product layout with up to 64 rows, with more and with
+    more than 1024, in stretches that items share, that they begin and alone."""
+    import torch
+    say(f"[range] attention {dt} D={D} G={G} T={T} {cut}")
+    kv, ps = 2, 32
+    base = {40: [3500, 2900, 1200, 33], 150: [1300, 900, 65, 7], 70: [300, 150, 64, 1],
+            1030: [70, 40, 33, 1]}[T]
+    caches, tables, _, ks, vs = attend_inputs(T + D, base, -(-base[0] // ps) + 1, kv, G, D, ps, dt,
+                                              hf=D != 128)
+    rng = np.random.default_rng(T + G)
+    rows = rng.choice(4, T, p=[0.5, 0.3, 0.1, 0.1]).astype(np.int32)
+    lens = np.array([rng.integers(base[r] // 2 + 1, base[r] + 1) for r in rows], np.int32)
+    lens[rng.permutation(T)[:T // 12]] = 0
+    got, stretch = stretches(lens, kv, G, D, tables.shape[1] * ps)
+    assert got == cut
+    if cut == "shared":   # of which many hold the end of one item and the start of another
+        ends = np.cumsum(np.repeat(-(-lens // 32), kv * (-(-G // 16))))
+        assert ((ends % stretch) != 0).sum() > len(lens)
+    q = rng.normal(0, 1, (T, kv * G * D)).astype(np.float32)
+    cache = tb.KvCache(*caches)
+    first = None
+    for _ in range(2):
+        out, lse = tb.bitnet_paged_attention(cache, 1, dev(q), dev(tables), dev(lens),
+                                             rows=dev(rows), return_lse=True)
+        assert first is None or torch.equal(first, out)
+        first = out
+    check_rows(host(out), host(lse), q, rows, lens, ks, vs, D ** -0.5, D, LOST[dt])
