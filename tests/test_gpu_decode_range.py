@@ -141,3 +141,137 @@ def test_attention_in_every_variant(tb, dt, D, G, cut, T):  # noqa: F811
         assert first is None or torch.equal(first, out)
         first = out
     check_rows(host(out), host(lse), q, rows, lens, ks, vs, D ** -0.5, D, LOST[dt])
+
+
+# ---- beam selection: streams of many tiles ---------------------------------------
+
+TILE = 4096
+
+
+def tiles_of(rows, V):
+    """Tiles that a workgroup takes one after the other, by the rule at the kernel's
+    plan."""
+    every = -(-V // TILE)
+    return -(-every // min(every, 64, -(-1024 // rows)))
+
+
+def select_exactly(x, scores, W, finished, eos):
+    """The definition for large vocabularies, fp64; and the smallest gap between
+    scores of different beams, up to the first that is left out."""
+    R, V = x.shape
+    out = {"scores": np.empty(R), "tokens": np.empty(R, np.int32), "parents": np.empty(R, np.int32),
+           "finished": np.empty(R, np.int32)}
+    gap = np.inf
+    for g in range(0, R, W):
+        cand = []
+        for r in range(g, g + W):
+            base = float(scores[r])
+            if finished[r]:
+                cand.append((-base, r, 0.0, eos))
+                cand += [(np.inf, r, 0.0, t) for t in range(W + 1) if t != eos]
+                continue
+            y = np.where(x[r] < np.inf, x[r], -np.inf)
+            m = np.float64(y.max())
+            lse = m + np.log(np.exp(y.astype(np.float64) - m).sum()) if m > -np.inf else 0.0
+            at = np.flatnonzero(y >= np.partition(y, V - W)[V - W])
+            at = at[np.argsort(-y[at], kind="stable")][:W]
+            cand += [(-(base + (np.float64(y[t]) - lse)), r, -y[t], int(t)) for t in at]
+        cand.sort()
+        for a, b in zip(cand[:W], cand[1:W + 1]):
+            if a[1] != b[1] and a[0] < np.inf and a[0] != b[0]:
+                gap = min(gap, b[0] - a[0])
+        for j, (s, r, _, t) in enumerate(cand[:W]):
+            out["scores"][g + j], out["tokens"][g + j], out["parents"][g + j] = -s, t, r
+            out["finished"][g + j] = int(bool(finished[r]) or t == eos)
+    return out, gap
+
+
+# What a row's logits look like, by token.  "stairs": every tile is above all before
+# it, so that each replaces what the lists hold and raises the maximum; "rising": so
+# do a tile's threads, a few at a time, until the lists are cut; "clumps": so do all
+# the logits of a few threads, and the lists are cut again and again; "holes": whole
+# tiles, the first among them, with no token that can be taken, or NaN; "dust": one
+# logit a thread and behind it terms that fp32 sums lose.
+def pattern(kind, rng, R, W, V):
+    i = np.arange(V)
+    if kind == "random":
+        x = rng.normal(0, 2, (R, V))
+    elif kind == "rising":
+        x = i * (30.0 / V) + rng.uniform(0, 8, (R, 1))
+    elif kind == "falling":
+        x = -i * (30.0 / V) + rng.uniform(0, 8, (R, 1))
+    elif kind == "stairs":
+        x = i // TILE * 1.5 + rng.random((R, V))
+    elif kind == "clumps":   # (a thread's logits are four by four, 1024 apart)
+        few = rng.random((R, -(-V // TILE), 256)) < (0.75 * min(max(W, 8), 32) / 64)
+        x = np.where(few[:, i // TILE, i % 1024 // 4], i // TILE * 1.5, -3.0) + rng.random((R, V))
+    elif kind == "equal":
+        x = np.repeat(rng.normal(0, 2, (R, 1)), V, 1)
+    elif kind == "holes":
+        x = rng.normal(0, 2, (R, V))
+        for r in range(R):
+            gone = rng.random(-(-V // TILE)) < 0.5
+            gone[0] = True
+            x[r, np.repeat(gone, TILE)[:V]] = (-np.inf, np.nan, np.inf)[r % 3]
+    else:
+        x = np.where(i < 1024, 0.0, -18.1) + rng.uniform(0, 1e-3, (R, V))
+    return np.ascontiguousarray(x, np.float32)
+
+
+SHAPES = [(32, 8, 151936), (8, 8, 151936), (256, 4, 20000), (70, 3, 65537), (700, 1, 30001),
+          (32, 32, 40000), (12, 12, 151936), (22, 12, 70000)]
+KINDS = ["random", "rising", "falling", "stairs", "clumps", "equal", "holes", "dust"]
+
+
+def stream_inputs(shape, kind):
+    B, W, V = shape
+    rng = np.random.default_rng(B * 37 + W + KINDS.index(kind))
+    x = pattern(kind, rng, B * W, W, V)
+    scores = (-3 - 9 * rng.random(B * W)).astype(np.float32)
+    finished = (rng.random(B * W) < 0.1).astype(np.int32) * 3
+    return x, scores, finished, int(rng.integers(0, V))
+
+
+def sum_error(rows, V):
+    """Relative error of a row's sum of exp in fp32, in units of u = 2^-24, and so the
+    absolute error of its logarithm.  The arguments' roundings, u times the distance
+    to the largest logit, weigh up to ln V on average; the constant log2 e is off
+    by less than u, which again counts up to ln V; an exponential 2 u, one for the
+    term and one for each of a thread's n - 1 and the two joins' rescalings; 4
+    for the sum of 16, two for each further tile (a product and a sum), one
+    for the rescaling to the chunk's maximum, 8 for the sums over lanes and
+    waves."""
+    n = tiles_of(rows, V)
+    return 2 * np.log(V) + 2 * (n + 2) + 4 + 2 * (n - 1) + 1 + 8
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_select_streams_of_many_tiles(tb, shape, kind):  # noqa: F811
+    import torch
+    B, W, V = shape
+    say(f"[range] selection B={B} W={W} V={V} {kind}")
+    R = B * W
+    assert tiles_of(R, V) >= 2
+    x, scores, finished, eos = stream_inputs(shape, kind)
+    want, gap = select_exactly(x, scores, W, finished, eos)
+    err = U * sum_error(R, V)
+    assert gap > 2 * err
+    xd, sd, fd = dev(x), dev(scores), dev(finished)
+    ws = torch.zeros(tb.bitnet_beam_select_workspace_bytes(B, W, V), dtype=torch.uint8, device="cuda:0")
+    first = None
+    for _ in range(2):
+        out = [torch.empty(R, device="cuda:0")] + [
+            torch.empty(R, dtype=torch.int32, device="cuda:0") for _ in range(3)]
+        tb.bitnet_beam_select_into(B, W, V, xd, sd, fd, eos, *out, ws)
+        got = [host(t) for t in out]
+        for a, n in zip(got[1:], ("tokens", "parents", "finished")):
+            assert np.array_equal(a, want[n]), n
+        s, exact = got[0].astype(np.float64), want["scores"]
+        inf = exact == -np.inf
+        assert np.array_equal(s == -np.inf, inf)
+        off = np.abs(s[~inf] - exact[~inf])
+        assert (off <= U * np.abs(exact[~inf]) + err).all(), float(off.max() / U)
+        assert first is None or first == got[0].tobytes()
+        first = got[0].tobytes()
+    say(f"  off by up to {float(off.max() / U):.1f} u of {err / U:.0f} + the rounding")
