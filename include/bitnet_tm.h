@@ -573,7 +573,15 @@ typedef struct bitnet_kv_pool {
  *   pages: the needs of the requests up to r, those with status 1 left out,
  *   exceed the stack; 3 the same for tokens and T.  (2 never meets a request
  *   that needs no page, 3 none that adds no token.)  A request that is not
- *   granted keeps its length and adds nothing.
+ *   granted keeps its length and adds nothing, and as long as its new_lens asks
+ *   for more than there is, so do those behind it that need pages (or tokens).
+ *   With state_out apart from state_in a step can be taken back: of the pool
+ *   nothing changes that state_in counts (table entries of its lengths, owned
+ *   pages, the stack up to its height), so the step may be mapped again from
+ *   state_in with other new_lens, as if the first call had not been.
+ *   The beams of a group (bitnet_beam_select) have to advance together, and end
+ *   together, since a beam's table may hold pages that another one owns: where
+ *   not all of a group are granted, map the step again with 0 for the group.
  *   Outputs: starts int32 [rows + 1], the tokens granted before each request;
  *   for the tokens in request order slots, positions and rows int32 [T]: slot
  *   in the cache, position in the request, request.  Entries behind the last
