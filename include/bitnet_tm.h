@@ -632,9 +632,10 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, int32_t layer, int6
  *   logarithm of the softmax's denominator.  Sums, maxima and outputs are held
  *   in fp32; queries and probabilities meet the cache's values on the matrix
  *   cores as sums of two or three 16-bit terms that together carry fp32's
- *   precision (for fp16 and int8 caches down to 2^-38 of a head's largest
- *   query channel, and of the largest probability, times the largest value
- *   scale; what lies below counts as zero).
+ *   precision (for bf16 caches down to 2^-126; for fp16 and int8 caches down
+ *   to 2^-38 of a head's largest query channel, and of the largest
+ *   probability, times the largest value scale; what lies below counts as
+ *   zero).
  *   tables int32 [table_rows][max_pages].  lens is clamped to [0, max_len];
  *   max_len <= max_pages * page_size is the host's bound, which sizes the
  *   split of the length.  A token whose page is outside [0, pages) is left
@@ -646,8 +647,8 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, int32_t layer, int6
  *   heads per kv head) and max_pages below 2^31, max_len below 2^30; q and out
  *   16-byte aligned, q_stride a multiple of 4 and below 2^31.
  *   q and the tokens in use are finite, scale is finite (else BITNET_ERR_SHAPE),
- *   and scale * q stays below 2^125; rows that break this give unspecified
- *   outputs of their own and leave the others alone.
+ *   and scale * q and scale * sum_i |q_i k_ji| stay below 2^125; rows that
+ *   break this give unspecified outputs of their own and leave the others alone.
  *   T == 0 launches nothing.  out, lse and workspace must overlap neither each
  *   other, nor the inputs, nor the layer.
  *   workspace: bitnet_paged_attention_workspace_bytes(...) bytes, 256-byte

@@ -99,7 +99,7 @@ def check_rows(out, lse, q, rows, lens, ks, vs, scale, D, lost):
             total = p.sum(1, keepdims=True)
             e = (m + np.log(total))[:, 0]
             p /= total
-            size = (scale * (np.abs(q[t, h]) @ kabs[rows[t]][h, :n].T)).max(1)
+            size = (abs(scale) * (np.abs(q[t, h]) @ kabs[rows[t]][h, :n].T)).max(1)
             tol = U * (2 * (D + 16) * size + 2 * n + 64)[:, None] * (p @ vabs[rows[t]][h, :n])
             tol += n * lost * vabs[rows[t]][h, :n].max()
             err = np.abs(out[t, h] - p @ v)
@@ -141,6 +141,56 @@ def test_attention_in_every_variant(tb, dt, D, G, cut, T):  # noqa: F811
         assert first is None or torch.equal(first, out)
         first = out
     check_rows(host(out), host(lse), q, rows, lens, ks, vs, D ** -0.5, D, LOST[dt])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "int8"])
+@pytest.mark.parametrize("T,kv,G,longest", [(3, 96, 1, 600), (2, 256, 2, 60), (70, 70, 2, 90),
+                                            (5, 70, 20, 130), (66, 40, 33, 200)])
+def test_attention_of_many_items_a_row(tb, dt, T, kv, G, longest):  # noqa: F811
+    """More than 64 key/value heads (times groups of 16 query heads) a row."""
+    D, ps = 64, 16
+    say(f"[range] attention {dt} T={T} kv={kv} G={G}")
+    base = [longest, longest // 2 + 1, 33]
+    caches, tables, _, ks, vs = attend_inputs(kv, base, -(-longest // ps), kv, G, D, ps, dt)
+    rng = np.random.default_rng(T)
+    rows = rng.integers(0, 3, T).astype(np.int32)
+    lens = np.array([rng.integers(1, base[r] + 1) for r in rows], np.int32)
+    lens[T // 2] = 0
+    q = rng.normal(0, 1, (T, kv * G * D)).astype(np.float32)
+    out, lse = tb.bitnet_paged_attention(tb.KvCache(*caches), 1, dev(q), dev(tables), dev(lens),
+                                         rows=dev(rows), return_lse=True)
+    check_rows(host(out), host(lse), q, rows, lens, ks, vs, D ** -0.5, D, LOST[dt])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "int8"])
+@pytest.mark.parametrize("scale", [0.0, -0.0, -0.25, 1e-30, -3.0])
+def test_attention_of_any_scale(tb, dt, scale):  # noqa: F811
+    say(f"[range] attention {dt} scale {scale}")
+    kv, G, D, ps = 2, 3, 128, 16
+    caches, tables, q, ks, vs = attend_inputs(4, [300, 65, 1], 20, kv, G, D, ps, dt)
+    lens = np.array([300, 65, 1], np.int32)
+    out, lse = tb.bitnet_paged_attention(tb.KvCache(*caches), 1, dev(q), dev(tables), dev(lens),
+                                         scale=scale, return_lse=True)
+    check_rows(host(out), host(lse), q, np.arange(3), lens, ks, vs, scale, D, LOST[dt])
+
+
+@pytest.mark.parametrize("q2,k2,v2", [(-100, 100, 0), (118, -118, 0), (100, -100, -110), (0, 0, 120),
+                                      (58, 58, 0), (50, 50, 100)])
+def test_attention_of_any_magnitude(tb, q2, k2, v2):  # noqa: F811
+    """bf16 caches near the ends of fp32: queries 2^-100 to 2^118, scores up to 2^122."""
+    import torch
+    say(f"[range] attention of q 2^{q2}, k 2^{k2}, v 2^{v2}")
+    kv, G, D, ps, lens = 2, 3, 64, 16, np.array([70, 33, 600], np.int32)
+    caches, tables, q, ks, vs = attend_inputs(6, lens.tolist(), 40, kv, G, D, ps, "bf16")
+    for c, f, vals in ((caches[0], k2, ks), (caches[1], v2, vs)):
+        c.copy_(torch.ldexp(c.float(), torch.tensor(f, device="cuda:0")).bfloat16())
+        for x in vals:
+            x *= 2.0 ** f
+    q *= np.float32(2.0 ** q2)
+    scale = 0.125
+    out, lse = tb.bitnet_paged_attention(tb.KvCache(*caches), 1, dev(q), dev(tables), dev(lens),
+                                         scale=scale, return_lse=True)
+    check_rows(host(out), host(lse), q, np.arange(3), lens, ks, vs, scale, D, LOST["bf16"])
 
 
 # ---- beam selection: streams of many tiles ---------------------------------------
