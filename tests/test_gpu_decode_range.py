@@ -325,3 +325,106 @@ def test_select_streams_of_many_tiles(tb, shape, kind):  # noqa: F811
         assert first is None or first == got[0].tobytes()
         first = got[0].tobytes()
     say(f"  off by up to {float(off.max() / U):.1f} u of {err / U:.0f} + the rounding")
+
+
+# ---- the largest sizes that are accepted ------------------------------------------
+
+def test_select_of_the_largest_vocabulary(tb):  # noqa: F811
+    """2^30 - 1 logits, rows 2^31 - 1 apart: 4096 tiles a thread."""
+    import torch
+    V, ld, W = (1 << 30) - 1, (1 << 31) - 1, 2
+    say("[range] selection of 2^30 - 1 logits")
+    x = torch.empty(ld + V, device="cuda:0")
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(3)
+    rows = [x[r * ld:r * ld + V] for r in range(W)]
+    best = [[V - 1, 5, V // 2], [V // 3, V - 2, 0]]
+    lse = []
+    for row, b in zip(rows, best):
+        for part in row.split(1 << 26):
+            part.copy_(torch.randn(part.numel(), generator=gen, device="cuda:0"))
+        row[torch.tensor(b, device="cuda:0")] = torch.tensor([9.0, 8.5, 8.0], device="cuda:0")
+        total = sum(float(part.double().exp().sum()) for part in row.split(1 << 26))
+        lse.append(np.log(total))
+    scores = np.array([-1, -1.25], np.float32)
+    cand = sorted((-(float(s) + v - e), b) for s, e, bs in zip(scores, lse, best)
+                  for v, b in zip((9.0, 8.5, 8.0), bs))
+    ws = torch.zeros(tb.bitnet_beam_select_workspace_bytes(1, W, V), dtype=torch.uint8, device="cuda:0")
+    s = torch.empty(W, device="cuda:0")
+    t, p = (torch.empty(W, dtype=torch.int32, device="cuda:0") for _ in range(2))
+    tb.bitnet_beam_select_into(1, W, V, torch.as_strided(x, (W, V), (ld, 1)), dev(scores), None, 0,
+                               s, t, p, None, ws)
+    err = U * sum_error(W, V)
+    assert host(t).tolist() == [b for _, b in cand[:W]]
+    off = np.abs(host(s).astype(np.float64) - [-c for c, _ in cand[:W]])
+    say(f"  off by up to {off.max() / U:.0f} u of {err / U:.0f}")
+    assert (off <= U * 32 + err).all()
+    assert [b in best[r] for r, b in zip(host(p).tolist(), host(t).tolist())] == [True] * W
+
+
+def test_map_of_the_most_tokens(tb):  # noqa: F811
+    """Room for 2^31 - 1 tokens, of which few are there: the rest is -1."""
+    import torch
+    T, B, ps, mp = (1 << 31) - 1, 3, 1024, 2
+    say("[range] map of 2^31 - 1 tokens")
+    pool, state = tb.KvPool.empty(B, mp, 8, ps)
+    new = np.array([2000, 0, 1500], np.int32)
+    out = tb.bitnet_kv_map(pool, T, dev(new), state)
+    assert host(out["starts"]).tolist() == [0, 2000, 2000, 3500]
+    want = np.concatenate([np.arange(2000), np.arange(1500)])
+    assert np.array_equal(host(out["positions"][:3500]), want)
+    slots = host(out["slots"][:3500])
+    assert np.array_equal(slots, np.repeat(host(pool.tables)[[0, 2]], 1024, 1).reshape(-1)[
+        np.concatenate([np.arange(2000), 2048 + np.arange(1500)])] * ps + want % ps)
+    for n in ("slots", "positions", "rows"):
+        for part in out[n][3500:].split(1 << 28):
+            assert (part == -1).all().item(), n
+
+
+def test_append_of_the_most_tokens(tb):  # noqa: F811
+    import torch
+    T, D, ps = (1 << 23) - 1, 64, 1024
+    say("[range] append of 2^23 - 1 tokens")
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(4)
+    cache = tb.KvCache.empty(1, 1 << 13, 1, ps, D)
+    slots = torch.randperm(1 << 23, generator=gen, device="cuda:0")[:T].int()
+    slots[7] = -1
+    k, v = (torch.randn(T, D, generator=gen, device="cuda:0") for _ in range(2))
+    cache.k.zero_(), cache.v.zero_()
+    tb.bitnet_kv_append(cache, 0, k, v, slots)
+    for c, x in ((cache.k, k), (cache.v, v)):
+        want = torch.zeros(1 << 23, D, dtype=torch.bfloat16, device="cuda:0")
+        live = torch.arange(T, device="cuda:0") != 7
+        want[slots[live].long()] = x[live].bfloat16()
+        assert torch.equal(c.view(-1, D), want)
+
+
+def test_reorder_of_the_most_rows_and_layers(tb):  # noqa: F811
+    """4096 beams in 1024 layers, each beam's last page half filled."""
+    import torch
+    B, W, D, ps, layers = 128, 32, 64, 2, 1024
+    say("[range] reordering of 4096 beams in 1024 layers")
+    R = B * W
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(5)
+    cache = tb.KvCache.empty(layers, 2 * R, 1, ps, D, torch.int8)
+    for c in (cache.k, cache.v):
+        c.copy_(torch.randint(-128, 128, c.shape, generator=gen, device="cuda:0", dtype=torch.int8))
+    for c in (cache.k_scale, cache.v_scale):
+        c.copy_(torch.rand(c.shape, generator=gen, device="cuda:0"))
+    tables = torch.randperm(2 * R, generator=gen, device="cuda:0").int().view(R, 2)
+    beam = torch.randint(0, W, (B, W), generator=gen, device="cuda:0")
+    parents = (beam + W * torch.arange(B, device="cuda:0")[:, None]).reshape(-1).int()
+    lens = torch.full((R,), 3, dtype=torch.int32, device="cuda:0")
+    old = [c.clone() for c in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    out = tb.bitnet_beam_reorder(cache, tables, lens, parents, W)
+    par, last = parents.long(), tables[:, 1].long()
+    assert torch.equal(out[:, 0], tables[par, 0])
+    assert torch.equal(out[:, 1].long().view(B, W).sort(1).values, last.view(B, W).sort(1).values)
+    for c, o in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), old):
+        new = out[:, 1].long()
+        assert torch.equal(c[:, new, :, :1], o[:, last[par], :, :1])      # the token in use
+        assert torch.equal(c[:, :, :, 1], o[:, :, :, 1])                  # the other place
+        full = tables[:, 0].long()
+        assert torch.equal(c[:, full], o[:, full])
