@@ -716,6 +716,8 @@ class KvPool:
                  free_pages: torch.Tensor):
         for t, name in ((tables, "tables"), (owned, "owned"), (free_pages, "free_pages")):
             _dev(t, torch.int32, name)
+            if t.device != tables.device:
+                raise ValueError(f"{name} is on another device than tables")
         if tables.dim() != 2 or owned.shape != tables.shape or free_pages.numel() != pages:
             raise ValueError("tables and owned are [rows, max_pages], free_pages [pages]")
         self.tables, self.owned, self.free_pages = tables, owned, free_pages
