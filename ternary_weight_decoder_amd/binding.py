@@ -810,10 +810,12 @@ def _on(stream):
     return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
-def _here(dev: torch.device) -> None:
+def _here(dev: torch.device, stream=None) -> None:
     if dev.index is not None and dev.index != torch.cuda.current_device():
         raise ValueError(f"tensors of {dev}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"a stream of {stream.device}, but tensors of {dev}")
 
 
 def _arg(t: torch.Tensor, dtype, shape, dev: torch.device, name: str) -> None:
@@ -837,7 +839,7 @@ def bitnet_kv_map(pool: KvPool, T: int, new_lens: torch.Tensor, state: torch.Ten
     end a request) and state int32 [2*rows + 1], which is updated in place ->
     dict of starts [rows + 1], slots, positions, rows [T] and status [rows]."""
     dev = pool.tables.device
-    _here(dev)
+    _here(dev, stream)
     _arg(new_lens, torch.int32, (pool.rows,), dev, "new_lens")
     _arg(state, torch.int32, (2 * pool.rows + 1,), dev, "state")
     with _on(stream):
@@ -854,7 +856,7 @@ def bitnet_kv_append(cache: KvCache, layer: int, k: torch.Tensor, v: torch.Tenso
     cos and sin [max_pos, head_dim/2] k and q [T, q_heads*head_dim] are rotated
     by their positions first.  Returns the rotated q (None without q)."""
     dev, D = cache.k.device, cache.head_dim
-    _here(dev)
+    _here(dev, stream)
     T = k.shape[0]
     _rows_arg(k, T, cache.kv_heads * D, dev, "k")
     _rows_arg(v, T, cache.kv_heads * D, dev, "v")
@@ -884,7 +886,7 @@ def bitnet_paged_attention(cache: KvCache, layer: int, q: torch.Tensor, tables: 
     what a table holds, scale to head_dim**-0.5.  Returns fp32 [T,
     q_heads*head_dim] (and the log-sum-exp [T, q_heads])."""
     dev, D = cache.k.device, cache.head_dim
-    _here(dev)
+    _here(dev, stream)
     T, width = q.shape
     _rows_arg(q, T, width, dev, "q")
     if width % (cache.kv_heads * D):
@@ -915,7 +917,7 @@ def bitnet_beam_select(logits: torch.Tensor, scores: torch.Tensor, W: int, finis
     scores [B*W], optional finished flags int32 [B*W] with the end token eos ->
     dict of scores, tokens, parents (row numbers) and, with finished, finished."""
     dev = logits.device
-    _here(dev)
+    _here(dev, stream)
     R, V = logits.shape
     _rows_arg(logits, R, V, dev, "logits")
     if W < 1 or R % W:
@@ -940,7 +942,7 @@ def bitnet_beam_reorder(cache: KvCache, tables: torch.Tensor, lens: torch.Tensor
     (row numbers); partly filled last pages are copied inside the cache.
     Returns new tables; the old ones are unchanged."""
     dev = cache.k.device
-    _here(dev)
+    _here(dev, stream)
     if tables.dim() != 2 or W < 1 or tables.shape[0] % W:
         raise ValueError("tables must be [B*W, max_pages]")
     R = tables.shape[0]

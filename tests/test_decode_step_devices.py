@@ -54,3 +54,23 @@ def test_cache_of_two_devices(devices):
     ok = [OnDevice(1, *shape, dtype=torch.int8) for _ in range(2)] + [
         OnDevice(1, *shape[:4], dtype=torch.float32) for _ in range(2)]
     assert tb.KvCache(*ok).kv_heads == 2
+
+
+def test_stream_of_another_device(monkeypatch):
+    """Each call refuses a stream that is not of its tensors' device, before it
+    allocates or launches anything."""
+    from types import SimpleNamespace
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    shape = (1, 4, 2, 16, 64)
+    cache = tb.KvCache(*(OnDevice(0, *shape, dtype=torch.bfloat16) for _ in range(2)))
+    pool = tb.KvPool(8, 16, OnDevice(0, 2, 4), OnDevice(0, 2, 4), OnDevice(0, 8))
+    f32 = lambda *s: OnDevice(0, *s, dtype=torch.float32)
+    i32 = lambda *s: OnDevice(0, *s)
+    other = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    for call in (lambda s: tb.bitnet_kv_map(pool, 4, i32(2), i32(5), stream=s),
+                 lambda s: tb.bitnet_kv_append(cache, 0, f32(3, 128), f32(3, 128), i32(3), stream=s),
+                 lambda s: tb.bitnet_paged_attention(cache, 0, f32(2, 128), i32(2, 4), i32(2), stream=s),
+                 lambda s: tb.bitnet_beam_select(f32(4, 100), f32(4), 2, stream=s),
+                 lambda s: tb.bitnet_beam_reorder(cache, i32(4, 4), i32(4), i32(4), 2, stream=s)):
+        with pytest.raises(ValueError, match="stream"):
+            call(other)
