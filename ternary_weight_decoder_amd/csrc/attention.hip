@@ -36,10 +36,13 @@
 // instead; its score becomes -inf and its value zero, whatever memory holds.
 //
 // Measured (2 key/value heads of 128 channels, 12 query heads, inputs rotating,
-// a launch in a graph): 64 bf16 rows of 1800-32,768 tokens 184-187 us, 6.1 TB/s,
-// reads within 0.5% of the cache's bytes, waves waiting 26% of their time; one
-// fp16 row of 32,767 tokens 17.3 us; 16 int8 rows of 225-1801 tokens 11.4; one
-// row of 257 tokens 9.3, a chain of fetches that a launch (1.8 us) begins.
+// a launch in a graph): 64 bf16 rows of 1800-32,768 tokens, 1066 MB, 178-203 us
+// from one device to the next, 5.3-6.0 TB/s, reads within 0.5% of the cache's
+// bytes, waves waiting 26% of their time; one fp16 row of 32,767 tokens 17.2-17.5
+// us; 16 int8 rows of 225-1801 tokens 11.4; one row of 257 tokens 9.4-9.6, a chain
+// of fetches that a launch (1.8 us) begins.  The same with 64 channels and 4
+// key/value heads: 64 rows of 16,384 tokens 192 us in 16 bits, 5.6 TB/s, 112 in 8
+// bits, 5.1.
 #include <algorithm>
 
 #include "bitnet_device.hpp"
