@@ -86,6 +86,13 @@ __device__ __forceinline__ int wave_sum(int v) {
   return v;
 }
 
+__device__ __forceinline__ float absmax4(f32x4 v) {
+  return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+}
+
+// Scale of an 8-bit row whose largest magnitude is a.
+__device__ __forceinline__ float scale_of(float a) { return (a == 0.0f) ? 1.0f : 127.0f / a; }
+
 // Round half to even, then clamp to [-127, 127] (v_rndne_f32 + v_med3).
 __device__ __forceinline__ int quant_one(float x, float s) {
   float p = x * s;

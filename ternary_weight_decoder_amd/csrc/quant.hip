@@ -56,12 +56,6 @@ struct QuantShared {
   int ired[kRowsPerBlock];
 };
 
-__device__ __forceinline__ float absmax4(f32x4 v) {
-  return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-}
-
-__device__ __forceinline__ float scale_of(float a) { return (a == 0.0f) ? 1.0f : 127.0f / a; }
-
 // Quantize 4 values at input index 4*i; returns their sum and stores them.
 __device__ __forceinline__ int quant_store4(f32x4 v, float s, int i, const RowOut &o) {
   const int q0 = quant_one(v.x, s), q1 = quant_one(v.y, s);
