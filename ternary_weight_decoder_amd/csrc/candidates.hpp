@@ -40,13 +40,21 @@ __device__ __forceinline__ float logit_of(u64 key) {
   const uint32_t o = (uint32_t)(key >> 32);
   return __builtin_bit_cast(float, o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
 }
-// exp2 of the difference of two maxima's exponents, m <= n, n > -inf.
-__device__ __forceinline__ bool huge(float m) { return fabsf(m) > 0x1p126f; }
-__device__ __forceinline__ float shift(float m, float n) {
-  return __builtin_amdgcn_exp2f(huge(n) ? (m - n) * kLog2e : m * kLog2e - n * kLog2e);
-}
+// The exponent that a maximum m stands for in units of log 2, whose exp2 its sum of
+// exp is relative to: the rounded product, as one fma a logit takes it; of a large
+// m, whose product's rounding would be a factor of its own (2^(m / 2^24)), the
+// exact one, which goes with exp2((x - m) c).
+__device__ __forceinline__ bool huge(float m) { return fabsf(m) > 0x1p20f; }
 __device__ __forceinline__ double exponent(float m) {
   return huge(m) ? (double)m * (double)kLog2e : (double)(m * kLog2e);
+}
+// The difference of two maxima's exponents, m <= n, n > -inf, and its exp2.
+__device__ __forceinline__ float rise(float m, float n) {
+  if (huge(n) || (huge(m) && m > -INFINITY)) return (float)(exponent(m) - exponent(n));
+  return m * kLog2e - n * kLog2e;
+}
+__device__ __forceinline__ float shift(float m, float n) {
+  return __builtin_amdgcn_exp2f(rise(m, n));
 }
 __device__ __forceinline__ uint32_t token_of(u64 key) { return 0xffffffffu - (uint32_t)key; }
 
