@@ -492,6 +492,7 @@ bitnet_status bitnet_ternary_matmul_stages(int64_t M, const bitnet_problem *prob
  *   bitnet_kv_map            pages, slots and positions of a step's tokens
  *   bitnet_kv_append         rotate q and k, write k and v into the pages
  *   bitnet_paged_attention   attention of one new token per row
+ *   bitnet_chunk_attention   attention of several new tokens per request
  *   bitnet_beam_select       the next beams (or greedy tokens) from the logits
  *   bitnet_beam_reorder      the pages of the selected beams
  * Lengths, page numbers and parents are DEVICE data that the host never
@@ -667,6 +668,43 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
                                      int64_t max_len, float scale, float *out, float *lse,
                                      void *workspace, size_t workspace_bytes, void *stream);
 
+/* bitnet_chunk_attention: the new tokens of R requests, as bitnet_kv_map and
+ *   bitnet_kv_append left them.  Rows starts[r] .. starts[r+1]-1 of q are the n
+ *   last of the lens[r] tokens that request r holds in the pages of table row
+ *   r; the i-th of them attends to the first lens[r] - n + i + 1:
+ *     out[t][h] = sum_j p_j v_j,  p = softmax_j(scale * q[t][h] . k_j),
+ *   heads, lse, precision and what has to be finite as bitnet_paged_attention
+ *   (which it equals within both calls' errors), except that an 8-bit value
+ *   whose scale is not finite counts as zero.  A token has no influence on rows
+ *   that come before it, whatever it holds.
+ *   starts int32 [R+1] (bitnet_kv_map's) and lens int32 [R] (its state's first
+ *   entries) are device data.  Starts are taken in ascending order (each as
+ *   the largest up to it) and clamped to [0, T], lengths to [0, max_len].  A
+ *   row that has no token to attend to gives zeros and lse -inf.  Rows of q
+ *   that are no request's (before the first start or behind the last) are not
+ *   read, and those of out and lse left as they are.
+ *   tables int32 [R][max_pages]; pages out of range, entries and slots behind
+ *   the length as for bitnet_paged_attention.
+ *   1 <= R <= BITNET_MAX_ROWS; T, heads, max_len, strides and alignment as for
+ *   bitnet_paged_attention.  T == 0 launches nothing.  out, lse and workspace
+ *   must overlap neither each other, nor the inputs, nor the layer.
+ *   workspace: bitnet_chunk_attention_workspace_bytes(...) bytes, 256-byte
+ *   aligned, its first 2 KB ZERO-FILLED before its first use and written by
+ *   nothing else (counters that every call leaves at zero; calls of any shapes
+ *   may follow each other on one workspace, none may overlap in time).  One
+ *   launch.
+ */
+size_t bitnet_chunk_attention_workspace_bytes(int64_t T, int64_t R, int64_t q_heads,
+                                              int64_t kv_heads, int64_t head_dim,
+                                              int64_t max_len);
+
+bitnet_status bitnet_chunk_attention(const bitnet_kv_cache *cache, int32_t layer, int64_t T,
+                                     int64_t q_heads, const float *q, int64_t q_stride, int64_t R,
+                                     const int32_t *starts, const int32_t *lens,
+                                     const int32_t *tables, int64_t max_pages, int64_t max_len,
+                                     float scale, float *out, float *lse, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
 /* bitnet_beam_select: the next W beams of each of B groups from the logits of
  *   its W beams, rows of fp32 [B*W][V], ld elements apart.  Candidate (beam w,
  *   token v) has the score scores_in[w] + logit - lse, lse the natural
@@ -725,6 +763,72 @@ bitnet_status bitnet_beam_reorder(const bitnet_kv_cache *cache, int64_t B, int64
                                   const int32_t *parents, const int32_t *lens,
                                   const int32_t *tables_in, int32_t *tables_out,
                                   int64_t max_pages, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Between the projections of a decoder layer, and behind the last.  The pages
+ * name neither the norms nor the activation of the decoder; these are those of
+ * its published architecture (root-mean-square norm before attention and
+ * before the feed-forward part, gate * sigmoid(gate) * up inside it).
+ * Outputs are fp32 rows y, 8-bit rows xq with a scale each, or both (at least one;
+ * NULL for the other; xq and x_scale go together): xq, x_scale are exactly
+ * bitnet_quant_act of y, the form bitnet_ternary_matmul_q8 takes (M > 16);
+ * the decode projections (M <= 16) take y.
+ *
+ * bitnet_add_rms_norm: h = fl32(x + residual) (residual NULL: h = x),
+ *     y = fl32(h * weight / sqrt(mean_k h^2 + eps)),
+ *   computed in fp64 and rounded once (off by half a unit in the last place
+ *   plus 2^-50 relative); a row with a zero under the root gives zeros.
+ *   sum_out (optional) takes h; it may be residual or x itself where their
+ *   rows are contiguous.
+ * bitnet_silu_mul: y = fl32(gate * up / (1 + exp(-gate))), in the same way
+ *   (2^-48); y may be gate or up itself where their rows are contiguous.
+ *
+ * x, residual, gate and up are fp32 rows of K values, their rows x_stride, ...
+ * elements apart; weight fp32 [K]; y, sum_out fp32 and xq int8 [M][K]
+ * contiguous; x_scale fp32 [M].  K a multiple of 4, 4..32768; M below 2^23;
+ * strides multiples of 4, at least K and below 2^31; pointers 16-byte aligned
+ * (x_scale 4).  eps finite, not negative.  Inputs (and x + residual) are
+ * finite; a row that breaks this gives unspecified outputs of its own.
+ * Outputs must not overlap each other or, apart from what is said above, the
+ * inputs.  M == 0 launches nothing.  One launch, no workspace.
+ * ------------------------------------------------------------------------ */
+bitnet_status bitnet_add_rms_norm(int64_t M, int64_t K, const float *x, int64_t x_stride,
+                                  const float *residual, int64_t residual_stride,
+                                  const float *weight, float eps, float *sum_out, float *y,
+                                  int8_t *xq, float *x_scale, void *stream);
+
+bitnet_status bitnet_silu_mul(int64_t M, int64_t K, const float *gate, int64_t gate_stride,
+                              const float *up, int64_t up_stride, float *y, int8_t *xq,
+                              float *x_scale, void *stream);
+
+/* bitnet_token_logprobs: of R rows of logits fp32 [R][V], ld elements apart,
+ *     lse = log sum_v exp(logit_v),   logprobs[r] = logit[tokens[r]] - lse,
+ *     entropy[r] = -sum_v p_v log p_v  (natural logarithms),
+ *   and the `top` largest in descending order, of equal ones the lower token
+ *   first: top_tokens int32, top_logprobs fp32 [R][top].
+ *   Logits of -inf are tokens that cannot be taken; NaN and +inf count as
+ *   -inf.  Of a row without any other logit lse counts as 0 (logprobs -inf) and
+ *   the entropy as 0.  A token outside [0, V) (a row that is padding, or has no
+ *   given token) gives logprobs 0.
+ *   tokens and logprobs may be NULL together, entropy may be NULL, with top
+ *   == 0 top_tokens and top_logprobs are; something has to be asked for.
+ *   The sums have fp32 terms and partial sums: lse and the log probabilities are
+ *   off by at most (15 + 4 n + 2 ln V) 2^-24 and one rounding, the entropy by
+ *   (1 + H + ln V) times as much, n = ceil(t / c), t = ceil(V / 4096),
+ *   c = min(t, 64, ceil(1024 / R)).
+ *   1 <= R <= 65535 (R == 0 launches nothing), 0 <= top <= 32, top <= V,
+ *   1 <= V < 2^30, V <= ld < 2^31; arrays 4-byte aligned.  Outputs and
+ *   workspace must not overlap each other or the inputs.
+ *   workspace: bitnet_token_logprobs_workspace_bytes(R, V, top) bytes, 256-byte
+ *   aligned, zero-filled before its first use, on the same terms as the
+ *   attention's.  One launch.
+ */
+size_t bitnet_token_logprobs_workspace_bytes(int64_t R, int64_t V, int64_t top);
+
+bitnet_status bitnet_token_logprobs(int64_t R, int64_t V, const float *logits, int64_t ld,
+                                    const int32_t *tokens, int64_t top, float *logprobs,
+                                    float *entropy, int32_t *top_tokens, float *top_logprobs,
+                                    void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

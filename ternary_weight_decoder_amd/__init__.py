@@ -14,6 +14,8 @@ _BINDING_NAMES = {
     "bitnet_ternarize_workspace_bytes", "bitnet_grouped_workspace_bytes",
     "KvCache", "KvPool", "bitnet_kv_map", "bitnet_kv_append", "bitnet_paged_attention",
     "bitnet_beam_select", "bitnet_beam_reorder",
+    "bitnet_chunk_attention", "bitnet_add_rms_norm", "bitnet_silu_mul", "bitnet_token_logprobs",
+    "bitnet_chunk_attention_workspace_bytes", "bitnet_token_logprobs_workspace_bytes",
     "bitnet_paged_attention_workspace_bytes", "bitnet_beam_select_workspace_bytes",
 }
 

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -19,6 +20,7 @@ LIB_PATH = _build.LIB_PATH
 
 BITNET_OK = 0
 BITNET_MAX_GROUP = 256
+CHUNK_COUNTERS = 2048   # zero-filled bytes at the head of a chunk attention workspace
 UNIT = 128
 
 _c = ctypes
@@ -155,6 +157,21 @@ def lib():
         L.bitnet_beam_select.restype = _i32
         L.bitnet_beam_reorder.argtypes = [_p, _i64, _i64, _p, _p, _p, _p, _i64, _p]
         L.bitnet_beam_reorder.restype = _i32
+        L.bitnet_chunk_attention_workspace_bytes.argtypes = [_i64] * 6
+        L.bitnet_chunk_attention_workspace_bytes.restype = _sz
+        L.bitnet_chunk_attention.argtypes = [_p, _i32, _i64, _i64, _p, _i64, _i64, _p, _p, _p,
+                                             _i64, _i64, _c.c_float, _p, _p, _p, _sz, _p]
+        L.bitnet_chunk_attention.restype = _i32
+        L.bitnet_add_rms_norm.argtypes = [_i64, _i64, _p, _i64, _p, _i64, _p, _c.c_float, _p, _p,
+                                          _p, _p, _p]
+        L.bitnet_add_rms_norm.restype = _i32
+        L.bitnet_silu_mul.argtypes = [_i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p]
+        L.bitnet_silu_mul.restype = _i32
+        L.bitnet_token_logprobs_workspace_bytes.argtypes = [_i64, _i64, _i64]
+        L.bitnet_token_logprobs_workspace_bytes.restype = _sz
+        L.bitnet_token_logprobs.argtypes = [_i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _p,
+                                            _sz, _p]
+        L.bitnet_token_logprobs.restype = _i32
         _lib = L
     return _lib
 
@@ -781,6 +798,23 @@ def bitnet_paged_attention_into(cache: KvCache, layer, T, q_heads, q, tables, le
            "bitnet_paged_attention")
 
 
+def bitnet_chunk_attention_workspace_bytes(T: int, R: int, q_heads: int, kv_heads: int,
+                                           head_dim: int, max_len: int) -> int:
+    return int(lib().bitnet_chunk_attention_workspace_bytes(T, R, q_heads, kv_heads, head_dim,
+                                                            max_len))
+
+
+def bitnet_chunk_attention_into(cache: KvCache, layer, T, q_heads, q, starts, lens, tables, max_len,
+                                scale, out, workspace, lse=None, stream=None) -> None:
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().bitnet_chunk_attention(cache.ref, layer, T, q_heads, _ptr(q),
+                                        _rows_stride(q, q_heads * cache.head_dim),
+                                        tables.size(0), _ptr(starts), _ptr(lens), _ptr(tables),
+                                        tables.size(1), max_len, scale, _ptr(out), _ptr(lse),
+                                        _ptr(workspace), ws_bytes, _stream(stream)),
+           "bitnet_chunk_attention")
+
+
 def bitnet_beam_select_workspace_bytes(B: int, W: int, V: int) -> int:
     return int(lib().bitnet_beam_select_workspace_bytes(B, W, V))
 
@@ -800,6 +834,36 @@ def bitnet_beam_reorder_into(cache: KvCache, B, W, parents, lens, tables_in, tab
     _check(lib().bitnet_beam_reorder(cache.ref, B, W, _ptr(parents), _ptr(lens), _ptr(tables_in),
                                      _ptr(tables_out), tables_in.size(1), _stream(stream)),
            "bitnet_beam_reorder")
+
+
+def bitnet_add_rms_norm_into(M, K, x, weight, eps, residual=None, sum_out=None, y=None, xq=None,
+                             x_scale=None, stream=None) -> None:
+    _check(lib().bitnet_add_rms_norm(M, K, _ptr(x), _rows_stride(x, K), _ptr(residual),
+                                     0 if residual is None else _rows_stride(residual, K),
+                                     _ptr(weight), eps, _ptr(sum_out), _ptr(y), _ptr(xq),
+                                     _ptr(x_scale), _stream(stream)),
+           "bitnet_add_rms_norm")
+
+
+def bitnet_silu_mul_into(M, K, gate, up, y=None, xq=None, x_scale=None, stream=None) -> None:
+    _check(lib().bitnet_silu_mul(M, K, _ptr(gate), _rows_stride(gate, K), _ptr(up),
+                                 _rows_stride(up, K), _ptr(y), _ptr(xq), _ptr(x_scale),
+                                 _stream(stream)),
+           "bitnet_silu_mul")
+
+
+def bitnet_token_logprobs_workspace_bytes(R: int, V: int, top: int = 0) -> int:
+    return int(lib().bitnet_token_logprobs_workspace_bytes(R, V, top))
+
+
+def bitnet_token_logprobs_into(R, V, logits, tokens, top, logprobs, entropy, top_tokens,
+                               top_logprobs, workspace, stream=None) -> None:
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().bitnet_token_logprobs(R, V, _ptr(logits), _rows_stride(logits, V), _ptr(tokens),
+                                       top, _ptr(logprobs), _ptr(entropy), _ptr(top_tokens),
+                                       _ptr(top_logprobs), _ptr(workspace), ws_bytes,
+                                       _stream(stream)),
+           "bitnet_token_logprobs")
 
 
 # Convenience forms: arguments checked against the cache's and the pool's
@@ -909,6 +973,110 @@ def bitnet_paged_attention(cache: KvCache, layer: int, q: torch.Tensor, tables: 
                                     D ** -0.5 if scale is None else scale, out, ws, rows, lse,
                                     stream)
     return (out, lse) if return_lse else out
+
+
+def bitnet_chunk_attention(cache: KvCache, layer: int, q: torch.Tensor, starts: torch.Tensor,
+                           lens: torch.Tensor, tables: torch.Tensor, max_len=None, scale=None,
+                           return_lse: bool = False, stream=None):
+    """Causal attention of the new tokens of R requests: rows starts[r] to
+    starts[r + 1] - 1 of q fp32 [T, q_heads*head_dim] are the last tokens of the
+    lens[r] that request r holds (its own among them) in the pages of table row
+    r.  starts int32 [R + 1], lens int32 [R]: as bitnet_kv_map's `starts` and
+    its state's first entries.  max_len defaults to what a table holds, scale to
+    head_dim**-0.5.  Returns fp32 [T, q_heads*head_dim] (and the log-sum-exp [T,
+    q_heads]); rows of q that are no request's give zeros (and -inf)."""
+    dev, D = cache.k.device, cache.head_dim
+    _here(dev, stream)
+    T, width = q.shape
+    _rows_arg(q, T, width, dev, "q")
+    if width % (cache.kv_heads * D):
+        raise ValueError("q's width must be a multiple of kv_heads*head_dim")
+    if tables.dim() != 2:
+        raise ValueError("tables must be [R, max_pages]")
+    R = tables.shape[0]
+    _arg(tables, torch.int32, tables.shape, dev, "tables")
+    _arg(starts, torch.int32, (R + 1,), dev, "starts")
+    _arg(lens, torch.int32, (R,), dev, "lens")
+    if max_len is None:
+        max_len = tables.shape[1] * cache.page_size
+    H = width // D
+    with _on(stream):
+        out = torch.zeros((T, width), dtype=torch.float32, device=dev)
+        lse = torch.full((T, H), -math.inf, device=dev) if return_lse else None
+        n = bitnet_chunk_attention_workspace_bytes(T, R, H, cache.kv_heads, D, max_len)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        ws[:CHUNK_COUNTERS].zero_()
+        bitnet_chunk_attention_into(cache, layer, T, H, q, starts, lens, tables, max_len,
+                                    D ** -0.5 if scale is None else scale, out, ws, lse, stream)
+    return (out, lse) if return_lse else out
+
+
+def bitnet_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual=None,
+                        codes: bool = False, stream=None):
+    """The root-mean-square norm of fp32 rows x [M, K] (rows may lie apart), with
+    `residual` of x + residual -> dict of y, or with `codes` of xq int8 and x_scale
+    as bitnet_ternary_matmul_q8 takes them, and with `residual` of their sum."""
+    dev = x.device
+    _here(dev, stream)
+    M, K = x.shape
+    _rows_arg(x, M, K, dev, "x")
+    _arg(weight, torch.float32, (K,), dev, "weight")
+    if residual is not None:
+        _rows_arg(residual, M, K, dev, "residual")
+    with _on(stream):
+        out = _row_outputs(M, K, dev, codes)
+        if residual is not None:
+            out["sum"] = torch.empty((M, K), dtype=torch.float32, device=dev)
+        bitnet_add_rms_norm_into(M, K, x, weight, eps, residual, out.get("sum"), out.get("y"),
+                                 out.get("xq"), out.get("x_scale"), stream)
+    return out
+
+
+def bitnet_silu_mul(gate: torch.Tensor, up: torch.Tensor, codes: bool = False, stream=None):
+    """gate * sigmoid(gate) * up of fp32 rows [M, K] (rows may lie apart, so both
+    may be halves of one tensor) -> dict of y, or with `codes` of xq and x_scale."""
+    dev = gate.device
+    _here(dev, stream)
+    M, K = gate.shape
+    _rows_arg(gate, M, K, dev, "gate")
+    _rows_arg(up, M, K, dev, "up")
+    with _on(stream):
+        out = _row_outputs(M, K, dev, codes)
+        bitnet_silu_mul_into(M, K, gate, up, out.get("y"), out.get("xq"), out.get("x_scale"),
+                             stream)
+    return out
+
+
+def _row_outputs(M: int, K: int, dev: torch.device, codes: bool):
+    if not codes:
+        return {"y": torch.empty((M, K), dtype=torch.float32, device=dev)}
+    return {"xq": torch.empty((M, K), dtype=torch.int8, device=dev),
+            "x_scale": torch.empty(M, dtype=torch.float32, device=dev)}
+
+
+def bitnet_token_logprobs(logits: torch.Tensor, tokens=None, top: int = 0, stream=None):
+    """fp32 logits [R, V] (rows may lie apart) -> dict of the entropy [R] in nats,
+    with tokens int32 [R] their logprobs [R] (0 for a token outside the
+    vocabulary), and with top > 0 the likeliest top_tokens and top_logprobs [R, top]."""
+    dev = logits.device
+    _here(dev, stream)
+    R, V = logits.shape
+    _rows_arg(logits, R, V, dev, "logits")
+    if tokens is not None:
+        _arg(tokens, torch.int32, (R,), dev, "tokens")
+    with _on(stream):
+        f32 = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)
+        out = {"entropy": f32(R)}
+        if tokens is not None:
+            out["logprobs"] = f32(R)
+        if top:
+            out["top_tokens"] = torch.empty((R, top), dtype=torch.int32, device=dev)
+            out["top_logprobs"] = f32(R, top)
+        ws = torch.zeros(bitnet_token_logprobs_workspace_bytes(R, V, top), dtype=torch.uint8,
+                         device=dev)
+        bitnet_token_logprobs_into(R, V, logits, tokens, top, out.get("logprobs"), out["entropy"],
+                                   out.get("top_tokens"), out.get("top_logprobs"), ws, stream)
+    return out
 
 
 def bitnet_beam_select(logits: torch.Tensor, scores: torch.Tensor, W: int, finished=None,

@@ -13,6 +13,7 @@
 #include "bitnet_internal.hpp"
 #include "bitnet_variants.hpp"
 #include "kv.hpp"
+#include "rows.hpp"
 #include "bitnet_tm.h"
 
 using namespace bitnet;
@@ -1100,6 +1101,69 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
   return from_hip(launch_attend(a, cache->dtype, cache->head_dim, as_stream(stream)));
 }
 
+// Shapes of an attention call over chunks, apart from the cache's own.
+static bool chunk_shape_ok(int64_t T, int64_t R, int64_t q_heads, int64_t kv_heads, int64_t D,
+                           int64_t max_len) {
+  return attend_shape_ok(T, q_heads, kv_heads, D, max_len) && R >= 1 && R <= kMaxRows;
+}
+
+size_t bitnet_chunk_attention_workspace_bytes(int64_t T, int64_t R, int64_t q_heads,
+                                              int64_t kv_heads, int64_t head_dim,
+                                              int64_t max_len) {
+  if (!chunk_shape_ok(T, R, q_heads, kv_heads, head_dim, max_len)) return 0;
+  return chunk_workspace_bytes(T, R, q_heads, kv_heads, head_dim, max_len);
+}
+
+bitnet_status bitnet_chunk_attention(const bitnet_kv_cache *cache, int32_t layer, int64_t T,
+                                     int64_t q_heads, const float *q, int64_t q_stride, int64_t R,
+                                     const int32_t *starts, const int32_t *lens,
+                                     const int32_t *tables, int64_t max_pages, int64_t max_len,
+                                     float scale, float *out, float *lse, void *workspace,
+                                     size_t workspace_bytes, void *stream) {
+  bitnet_status st = check_cache(cache, layer);
+  if (st != BITNET_OK) return st;
+  if (T == 0) return BITNET_OK;
+  if (!q || !starts || !lens || !tables || !out) return BITNET_ERR_NULL;
+  const int64_t D = cache->head_dim, qd = q_heads * D;
+  if (!chunk_shape_ok(T, R, q_heads, cache->kv_heads, D, max_len) || q_stride < qd ||
+      q_stride >= kLimit || max_pages < 1 || max_pages >= kLimit ||
+      max_len > max_pages * cache->page_size || !std::isfinite(scale))
+    return BITNET_ERR_SHAPE;
+  if (q_stride % 4 || !aligned(q, 16) || !aligned(out, 16) || !aligned(starts, 4) ||
+      !aligned(lens, 4) || !aligned(tables, 4) || (lse && !aligned(lse, 4)))
+    return BITNET_ERR_ALIGN;
+  const size_t need = chunk_workspace_bytes(T, R, q_heads, cache->kv_heads, D, max_len);
+  if (!workspace || workspace_bytes < need) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return BITNET_ERR_ALIGN;
+  const Range r[] = {{out, T * qd * 4},
+                     {lse, T * q_heads * 4},
+                     {workspace, (int64_t)need},
+                     {q, ((T - 1) * q_stride + qd) * 4},
+                     {tables, R * max_pages * 4},
+                     {starts, (R + 1) * 4},
+                     {lens, R * 4}};
+  if (overlaps_any(r, 3, 7) || overlaps_cache(cache, layer, 1, r, 3, 3)) return BITNET_ERR_ALIAS;
+  st = device_check();
+  if (st != BITNET_OK) return st;
+  ChunkArgs a;
+  a.c = kv_view(cache, layer);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.starts = starts;
+  a.lens = lens;
+  a.tables = tables;
+  a.T = (int32_t)T;
+  a.R = (int32_t)R;
+  a.q_heads = (int32_t)q_heads;
+  a.max_pages = (int32_t)max_pages;
+  a.max_len = (int32_t)max_len;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.ws = static_cast<uint8_t *>(workspace);
+  return from_hip(launch_chunk(a, cache->dtype, cache->head_dim, as_stream(stream)));
+}
+
 static bool beams_ok(int64_t B, int64_t W) {
   return B >= 1 && W >= 1 && W <= kMaxWidth && B <= kMaxRows && B * W <= kMaxRows;
 }
@@ -1186,6 +1250,143 @@ bitnet_status bitnet_beam_reorder(const bitnet_kv_cache *cache, int64_t B, int64
   a.tables_in = tables_in;
   a.tables_out = tables_out;
   return from_hip(launch_beam_reorder(a, as_stream(stream)));
+}
+
+// ---- rows between the projections, and token log probabilities ---------------
+
+// Fp32 rows of K values, `stride` elements apart.
+static bool row_stride_ok(int64_t stride, int64_t K) { return stride >= K && stride < kLimit; }
+static bool rows_shape_ok(int64_t M, int64_t K) {
+  return M >= 0 && M < kMaxTokens && K >= 4 && K <= kMaxRowWidth && K % 4 == 0;
+}
+
+bitnet_status bitnet_add_rms_norm(int64_t M, int64_t K, const float *x, int64_t x_stride,
+                                  const float *residual, int64_t residual_stride,
+                                  const float *weight, float eps, float *sum_out, float *y,
+                                  int8_t *xq, float *x_scale, void *stream) {
+  if (M == 0) return BITNET_OK;
+  if (!x || !weight || (!y && !xq) || (xq != nullptr) != (x_scale != nullptr))
+    return BITNET_ERR_NULL;
+  if (!rows_shape_ok(M, K) || !row_stride_ok(x_stride, K) ||
+      (residual && !row_stride_ok(residual_stride, K)) || !std::isfinite(eps) || eps < 0.0f)
+    return BITNET_ERR_SHAPE;
+  if (x_stride % 4 || (residual && residual_stride % 4) || !aligned(x, 16) ||
+      !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum_out, 16) ||
+      !aligned(y, 16) || !aligned(xq, 16) || !aligned(x_scale, 4))
+    return BITNET_ERR_ALIGN;
+  // The sum may take the place of one of its terms.
+  const bool on_x = sum_out == x && x_stride == K;
+  const bool on_r = sum_out == residual && residual_stride == K;
+  const Range r[] = {{sum_out, M * K * 4},
+                     {y, M * K * 4},
+                     {xq, M * K},
+                     {x_scale, M * 4},
+                     {on_x ? nullptr : x, ((M - 1) * x_stride + K) * 4},
+                     {on_r ? nullptr : residual, ((M - 1) * residual_stride + K) * 4},
+                     {weight, K * 4}};
+  if (overlaps_any(r, 4, 7)) return BITNET_ERR_ALIAS;
+  bitnet_status st = device_check();
+  if (st != BITNET_OK) return st;
+  NormArgs a;
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.sum = sum_out;
+  a.y = y;
+  a.xq = xq;
+  a.x_scale = x_scale;
+  a.x_stride = x_stride;
+  a.r_stride = residual_stride;
+  a.M = (int32_t)M;
+  a.K = (int32_t)K;
+  a.eps = eps;
+  return from_hip(launch_add_rms_norm(a, as_stream(stream)));
+}
+
+bitnet_status bitnet_silu_mul(int64_t M, int64_t K, const float *gate, int64_t gate_stride,
+                              const float *up, int64_t up_stride, float *y, int8_t *xq,
+                              float *x_scale, void *stream) {
+  if (M == 0) return BITNET_OK;
+  if (!gate || !up || (!y && !xq) || (xq != nullptr) != (x_scale != nullptr))
+    return BITNET_ERR_NULL;
+  if (!rows_shape_ok(M, K) || !row_stride_ok(gate_stride, K) || !row_stride_ok(up_stride, K))
+    return BITNET_ERR_SHAPE;
+  if (gate_stride % 4 || up_stride % 4 || !aligned(gate, 16) || !aligned(up, 16) ||
+      !aligned(y, 16) || !aligned(xq, 16) || !aligned(x_scale, 4))
+    return BITNET_ERR_ALIGN;
+  // y may take the place of one of its factors.
+  const bool on_g = y == gate && gate_stride == K, on_u = y == up && up_stride == K;
+  const Range r[] = {{y, M * K * 4},
+                     {xq, M * K},
+                     {x_scale, M * 4},
+                     {on_g ? nullptr : gate, ((M - 1) * gate_stride + K) * 4},
+                     {on_u ? nullptr : up, ((M - 1) * up_stride + K) * 4}};
+  if (overlaps_any(r, 3, 5)) return BITNET_ERR_ALIAS;
+  bitnet_status st = device_check();
+  if (st != BITNET_OK) return st;
+  GateArgs a;
+  a.gate = gate;
+  a.up = up;
+  a.y = y;
+  a.xq = xq;
+  a.x_scale = x_scale;
+  a.g_stride = gate_stride;
+  a.u_stride = up_stride;
+  a.M = (int32_t)M;
+  a.K = (int32_t)K;
+  return from_hip(launch_silu_mul(a, as_stream(stream)));
+}
+
+constexpr int64_t kMaxScored = 65535;   // rows: a grid's second axis
+static bool score_shape_ok(int64_t R, int64_t V, int64_t top) {
+  return R >= 1 && R <= kMaxScored && V >= 1 && V < kMaxVocab && top >= 0 && top <= kMaxWidth &&
+         top <= V;
+}
+
+size_t bitnet_token_logprobs_workspace_bytes(int64_t R, int64_t V, int64_t top) {
+  if (!score_shape_ok(R, V, top)) return 0;
+  return logprobs_workspace_bytes(R, V, top);
+}
+
+bitnet_status bitnet_token_logprobs(int64_t R, int64_t V, const float *logits, int64_t ld,
+                                    const int32_t *tokens, int64_t top, float *logprobs,
+                                    float *entropy, int32_t *top_tokens, float *top_logprobs,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
+  if (R == 0) return BITNET_OK;
+  if (!logits || (logprobs != nullptr) != (tokens != nullptr) ||
+      (top > 0) != (top_tokens != nullptr) || (top > 0) != (top_logprobs != nullptr))
+    return BITNET_ERR_NULL;
+  if (!logprobs && !entropy && top == 0) return BITNET_ERR_NULL;
+  if (!score_shape_ok(R, V, top) || ld < V || ld >= kLimit) return BITNET_ERR_SHAPE;
+  const void *ptrs[] = {logits, tokens, logprobs, entropy, top_tokens, top_logprobs};
+  for (const void *p : ptrs)
+    if (!aligned(p, 4)) return BITNET_ERR_ALIGN;
+  const size_t need = logprobs_workspace_bytes(R, V, top);
+  if (!workspace || workspace_bytes < need) return BITNET_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return BITNET_ERR_ALIGN;
+  const Range r[] = {{logprobs, R * 4},
+                     {entropy, R * 4},
+                     {top_tokens, R * top * 4},
+                     {top_logprobs, R * top * 4},
+                     {workspace, (int64_t)need},
+                     {logits, ((R - 1) * ld + V) * 4},
+                     {tokens, R * 4}};
+  if (overlaps_any(r, 5, 7)) return BITNET_ERR_ALIAS;
+  bitnet_status st = device_check();
+  if (st != BITNET_OK) return st;
+  LogprobArgs a;
+  a.logits = logits;
+  a.tokens = tokens;
+  a.logprobs = logprobs;
+  a.entropy = entropy;
+  a.top_tokens = top_tokens;
+  a.top_logprobs = top_logprobs;
+  a.ld = ld;
+  a.R = (int32_t)R;
+  a.V = (int32_t)V;
+  a.top = (int32_t)top;
+  a.ws = static_cast<uint8_t *>(workspace);
+  return from_hip(launch_token_logprobs(a, as_stream(stream)));
 }
 
 }  // extern "C"

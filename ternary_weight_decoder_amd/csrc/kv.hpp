@@ -66,6 +66,21 @@ size_t attend_workspace_bytes(int64_t T, int64_t q_heads, int64_t kv_heads, int6
                               int64_t max_len);
 hipError_t launch_attend(const AttendArgs &a, int dtype, int head_dim, hipStream_t stream);
 
+// chunk.hip
+struct ChunkArgs {
+  KvView c;
+  const float *q;
+  int64_t q_stride;
+  const int32_t *starts, *lens, *tables;
+  int32_t T, R, q_heads, max_pages, max_len;
+  float scale;
+  float *out, *lse;
+  uint8_t *ws;
+};
+size_t chunk_workspace_bytes(int64_t T, int64_t R, int64_t q_heads, int64_t kv_heads,
+                             int64_t head_dim, int64_t max_len);
+hipError_t launch_chunk(const ChunkArgs &a, int dtype, int head_dim, hipStream_t stream);
+
 // beam.hip
 struct SelectArgs {
   const float *logits, *scores_in;
