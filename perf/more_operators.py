@@ -327,7 +327,8 @@ def _plain_rows(y, codes):
     if not codes:
         return {"y": y}
     top = y.abs().amax(-1)
-    scale = torch.where(top == 0, 1.0, 127.0 / top)
+    # (a number over an fp32 tensor is a reciprocal and a product, rounded twice)
+    scale = torch.where(top == 0, 1.0, (127.0 / top.double()).float())
     q = torch.round(y * scale[:, None]).clamp(-127, 127).to(torch.int8)
     return {"x": torch.div(q, scale[:, None]), "scale": scale}
 
