@@ -689,10 +689,9 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
  *   bitnet_paged_attention.  T == 0 launches nothing.  out, lse and workspace
  *   must overlap neither each other, nor the inputs, nor the layer.
  *   workspace: bitnet_chunk_attention_workspace_bytes(...) bytes, 256-byte
- *   aligned, its first 2 KB ZERO-FILLED before its first use and written by
- *   nothing else (counters that every call leaves at zero; calls of any shapes
- *   may follow each other on one workspace, none may overlap in time).  One
- *   launch.
+ *   aligned; what it holds before does not matter, and nothing is kept in it
+ *   from one call to the next (calls that share it must not overlap in time).
+ *   Two launches.
  */
 size_t bitnet_chunk_attention_workspace_bytes(int64_t T, int64_t R, int64_t q_heads,
                                               int64_t kv_heads, int64_t head_dim,

@@ -20,7 +20,6 @@ LIB_PATH = _build.LIB_PATH
 
 BITNET_OK = 0
 BITNET_MAX_GROUP = 256
-CHUNK_COUNTERS = 2048   # zero-filled bytes at the head of a chunk attention workspace
 UNIT = 128
 
 _c = ctypes
@@ -1005,7 +1004,6 @@ def bitnet_chunk_attention(cache: KvCache, layer: int, q: torch.Tensor, starts: 
         lse = torch.full((T, H), -math.inf, device=dev) if return_lse else None
         n = bitnet_chunk_attention_workspace_bytes(T, R, H, cache.kv_heads, D, max_len)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        ws[:CHUNK_COUNTERS].zero_()
         bitnet_chunk_attention_into(cache, layer, T, H, q, starts, lens, tables, max_len,
                                     D ** -0.5 if scale is None else scale, out, ws, lse, stream)
     return (out, lse) if return_lse else out

@@ -31,6 +31,7 @@
 // item, whole ones and the beginning of another; the parts of an item are joined
 // by the workgroup that finishes last.
 #include <algorithm>
+#include <type_traits>
 
 #include "bitnet_device.hpp"
 #include "bitnet_internal.hpp"
@@ -42,32 +43,40 @@ namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
 constexpr int kCols = 32;                 // rows (token, head) of a wave
-constexpr int kRows = kCols * kWaves;     // of an item
-constexpr int kTile = 32;                 // tokens of a step
+constexpr int kRowWaves = 4;
+constexpr int kRows = kCols * kRowWaves;  // of an item
+constexpr int kBlock = 32;                // tokens of a wave's step
+// Two groups of waves take the blocks of a tile, and join in LDS at the end; with
+// 256 channels a wave fills its SIMD's registers, and there is one group.
+constexpr int split_of(int D) { return D == 256 ? 1 : 2; }
+constexpr int threads_of(int D) { return 64 * kRowWaves * split_of(D); }
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-constexpr int kGrid = 512;                // workgroups: two a compute unit
-constexpr int kHeaderBytes = 4 * kGrid;   // a counter for each
+constexpr int kGrid = 256;                // workgroups: one a compute unit
+constexpr int kFixed = 256;               // tokens that an item's beginning and end cost as much as
 constexpr int kLeast = 1;                 // tiles of a stretch, at least
 
 struct ChunkPlan {
   int groups;
-  size_t outs, stats, total;   // workspace offsets
+  size_t outs, stats, total;   // workspace offsets; records first
+};
+// Of a workgroup: the item whose first part it has.  Its parts' places are `place`,
+// then every second one from 2 (w + 1) on.
+struct Record {
+  int32_t parts, place, from, m0, count, kvh, pad[2];
 };
 
 ChunkPlan chunk_plan(int64_t T, int64_t R, int64_t q_heads, int64_t kv_heads, int64_t D,
                      int64_t max_len) {
   const int64_t items = kv_heads * (T * (q_heads / kv_heads) / kRows + R);
-  const int64_t tiles = (max_len + kTile - 1) / kTile;
+  const int64_t tile = kBlock * split_of((int)D), tiles = (max_len + tile - 1) / tile;
   ChunkPlan p;
-  p.groups = (int)std::min<int64_t>(D == 256 ? kGrid / 2 : kGrid, items * tiles);
+  p.groups = (int)std::min<int64_t>(kGrid, items * (tiles + kFixed / tile));
   // Two places a workgroup: for the item at its beginning and the one at its end.
   const size_t rows = 2 * (size_t)p.groups * kRows;
-  p.outs = kHeaderBytes;
+  p.outs = kGrid * sizeof(Record);
   p.stats = p.outs + rows * D * 4;
   p.total = p.stats + rows * 8;
   return p;
@@ -93,7 +102,7 @@ struct OperandF16 {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
   static __device__ __forceinline__ void split(const float (&x)[8], V (&t)[2]) {
-    terms_f16(x, t);
+    terms_f16_packed(x, t);
   }
 };
 template <> struct Operand<BITNET_KV_FP16> : OperandF16 { static constexpr int kBytes = 2; };
@@ -111,6 +120,15 @@ __device__ __forceinline__ float sum2(float v) {
   const auto p = __builtin_amdgcn_permlane32_swap(a, a, false, false);
   const uint32_t p0 = p[0], p1 = p[1];
   return __builtin_bit_cast(float, p0) + __builtin_bit_cast(float, p1);
+}
+
+// Maximum over the 32 lanes of a half that hold the same in both.
+__device__ __forceinline__ float across32(float v) {
+  v = across16<true>(v);
+  const uint32_t a = __builtin_bit_cast(uint32_t, v);
+  const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const uint32_t p0 = p[0], p1 = p[1];
+  return fmaxf(__builtin_bit_cast(float, p0), __builtin_bit_cast(float, p1));
 }
 
 // Inclusive sum and maximum over the wave.  Places on the line are whole numbers
@@ -142,10 +160,21 @@ __device__ __forceinline__ int scan_max(int v) {
   v = max_from<0x142, 0xA>(v);
   return max_from<0x143, 0xC>(v);
 }
-// floor(x / d) of whole numbers below 2^53.
-__device__ __forceinline__ double quotient(double x, double d) {
-  const double q = floor(x / d);
-  return q * d > x ? q - 1.0 : q;
+__device__ __forceinline__ double read_lane(double v, int i) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, i);
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), i);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// floor(x / d) of whole numbers, x below 2^53, the quotient below 2^30, inv = 1 / d
+// within 2^-40 (a division is thirty instructions, which a short call waits for).
+__device__ __forceinline__ double inverse(double d) {
+  const double r = __builtin_amdgcn_rcp(d);
+  return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
+__device__ __forceinline__ double quotient(double x, double d, double inv) {
+  const double q = floor(x * inv), r = __builtin_fma(-q, d, x);
+  return r < 0.0 ? q - 1.0 : r >= d ? q + 1.0 : q;
 }
 __device__ __forceinline__ double uniform(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
@@ -156,32 +185,90 @@ __device__ __forceinline__ double uniform(double v) {
 
 template <int DT, int D>
 struct ChunkShape {
+  static constexpr int kSplit = split_of(D), kTile = kBlock * kSplit;   // tokens of a step
+  static constexpr int kWaves = kRowWaves * kSplit, kThreads = threads_of(D);
   static constexpr int kBytes = Operand<DT>::kBytes;
   static constexpr int kPieces = D * kBytes / 16;             // of a cached row
-  static constexpr int kPass = kThreads / kPieces < kTile ? kThreads / kPieces : kTile;   // tokens
-  static constexpr int kLoads = kTile / kPass;                // of a thread, keys and values each
-  static constexpr int kRow = 2 * D + 16;                     // bytes of a row in LDS
+  static constexpr int kPass = 256 / kPieces < kBlock ? 256 / kPieces : kBlock;   // tokens
+  static constexpr int kLoads = kBlock / kPass;               // of a thread, keys and values each
+  static constexpr int kWaveTokens = 64 / kPieces;            // of a wave's load
+  // Bytes of a row in LDS: eight rows' pieces of keys, and the four rows that a
+  // transposing read takes of values, lie on banks of their own.
+  static constexpr int kKeyRow = 2 * D + 16, kValueRow = 2 * D + 32;
+  static constexpr int kMine = D / 32 / kSplit;               // channel blocks a wave ends up with
+  // Of three terms of the queries the smallest stays in LDS: registers are short.
+  static constexpr int kTerms = Operand<DT>::kTerms;
+  static constexpr int kKept = kTerms == 3 && D >= 128 ? 2 : kTerms;
 };
 
-template <int DT, int D>
+// A request's new tokens: rows [from, from + n) of q; `old` tokens lie before them
+// (may be negative).  Its rows (token, head) make `tiles` items for each key/value
+// head, on `line` places of the line.  An item has `lead` of them for the tokens
+// before the new ones and what its beginning and end cost.
+struct Request {
+  int from, n, old, tiles;
+  double lead, line;
+};
+template <int DT, int D, bool FEW>
 struct ChunkShared {
   typedef ChunkShape<DT, D> S;
-  __attribute__((aligned(16))) uint8_t k[2][kTile * S::kRow], v[2][kTile * S::kRow];
-  float scales[kWaves][2][kTile];   // 8-bit caches: the tile's key and value scales
-  double first[kThreads];           // places before each thread's requests
-  int top[kThreads];                // largest start before them
-  double wave_sum[kWaves];
-  int wave_top[kWaves];
-  uint32_t last;
+  // Of each group a block of keys, then one of values; in the end what the groups
+  // exchange.
+  static constexpr int kKeyBytes = kBlock * S::kKeyRow, kValueBytes = kBlock * S::kValueRow;
+  static constexpr int kBytes = std::max(S::kSplit * (kKeyBytes + kValueBytes),
+                                         (S::kSplit - 1) * S::kWaves * S::kMine * 4096);
+  __attribute__((aligned(16))) uint8_t kv[kBytes];
+  __attribute__((aligned(16))) uint8_t q[S::kKept < S::kTerms ? S::kWaves * 64 * D : 16];
+  float stats[S::kWaves][2][kCols];        // and their bases and sums
+  int pages[S::kWaves][64];
+  float scales[S::kWaves][2][2][kBlock];   // 8-bit caches: two blocks' key and value scales
+  double first[FEW ? 64 : S::kThreads];    // places before each request, or each thread's
+  Request request[FEW ? 64 : 1];
+  int top[FEW ? 1 : S::kThreads];          // largest start before them
+  double wave_sum[S::kWaves];
+  int wave_top[S::kWaves];
 };
 
 struct ChunkGrid {
-  int64_t outs_off, stats_off;
+  int64_t outs_off, stats_off;     // in the workspace
+  double over_groups, over_unit;   // 1 / workgroups, 1 / (a tile of tokens' places)
   int32_t groups, per;   // workgroups; query heads per key/value head
 };
 
-template <int DT, int D>
-__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
+// From the largest start up to this request's, which is the next one's at least.
+__device__ __forceinline__ Request request_of(const ChunkArgs &a, int per, int start, int next,
+                                              int len) {
+  Request q;
+  q.from = min(start, a.T);
+  q.n = min(max(start, next), a.T) - q.from;
+  q.old = min(max(len, 0), a.max_len) - q.n;
+  const int rows = q.n * per;
+  q.tiles = (rows + kRows - 1) / kRows;
+  q.lead = (double)(max(q.old, 0) + kFixed) * per;
+  q.line = q.tiles == 0 ? 0.0
+                        : q.tiles * q.lead + (double)(kRows / 2) * q.tiles * (q.tiles - 1) + rows;
+  return q;
+}
+
+// 16 of a row's 32 channels of a block, times `over`.
+__device__ __forceinline__ void store_block(float *out, const f32x16 &y, float over) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    st_global<f32x4>(out + 8 * e, f32x4{y[4 * e] * over, y[4 * e + 1] * over, y[4 * e + 2] * over,
+                                        y[4 * e + 3] * over});
+}
+// Exponent of the power of two above x >= 0, at least -100.
+__device__ __forceinline__ float exponent_above(float x) {
+  return (float)((int)(__builtin_bit_cast(uint32_t, pow2_above(x)) >> 23) - 127);
+}
+__device__ __forceinline__ float row_lse(float base, float sum) {
+  return sum > 0.0f ? (base + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// FEW: up to 64 requests, which every wave holds a lane each.
+// HALVES: 16 tokens in a row always lie on one page, at 32-bit offsets.
+template <int DT, int D, bool FEW, bool HALVES>
+__global__ void __launch_bounds__(threads_of(D)) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
 chunk_kernel(ChunkArgs a, ChunkGrid g) {
   typedef Operand<DT> F;
   typedef typename F::V V;
@@ -190,40 +277,37 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
   constexpr int kSteps = D / 16;       // contraction steps of the scores
   constexpr int kBlocks = D / 32;      // channel blocks of the outputs
   constexpr int kTerms = F::kTerms;
-  constexpr float kUp = F::kHalf ? 14.0f : 0.0f;   // probabilities are scaled by 2^kUp
-  __shared__ ChunkShared<DT, D> sh;
+  constexpr int kTile = S::kTile, kWaves = S::kWaves, kThreads = S::kThreads, kSplit = S::kSplit;
+  // Probabilities are relative to 2^-kUp of a base that the running maximum
+  // exceeds by up to 2^kSlack, so that it need not follow every new maximum.  With
+  // 8-bit values the maximum is that of probability times scale, and the values
+  // that the products take are bare codes.
+  constexpr float kSlack = 6.0f, kUp = F::kHalf ? 15.0f - kSlack : 0.0f;
+  typedef ChunkShared<DT, D, FEW> Sh;
+  __shared__ Sh sh;
 
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rw = wave % kRowWaves, part = wave / kRowWaves;   // 32 rows of an item; block of a tile
   const int per = g.per, kv_heads = a.c.kv_heads;
-
-  // A request's new tokens [from, to), the largest start so far being `top`
-  // (starts are taken in ascending order whatever they hold), and what it adds
-  // to the line for each key/value head.
-  struct Request {
-    int from, n, old, tiles;   // old: tokens before the new ones (may be negative)
-    double rows, lead, line;   // n * per; rows that lie before an item's own; places
-  };
-  auto request = [&](int r, int &top) {
-    top = max(top, ld_global<int>(a.starts + r));
-    Request q;
-    q.from = min(top, a.T);
-    const int to = min(max(top, ld_global<int>(a.starts + r + 1)), a.T);
-    q.n = to - q.from;
-    q.old = min(max(ld_global<int>(a.lens + r), 0), a.max_len) - q.n;
-    const int rows = q.n * per;
-    q.tiles = (rows + kRows - 1) / kRows;
-    q.rows = rows;
-    q.lead = (double)max(q.old, 0) * per;
-    q.line = q.tiles == 0 ? 0.0
-                          : q.tiles * q.lead + (double)(kRows / 2) * q.tiles * (q.tiles - 1) + q.rows;
-    return q;
-  };
 
   const int each = (a.R + kThreads - 1) / kThreads;
   const int r0 = min(tid * each, a.R), r1 = min(r0 + each, a.R);
   double total;
-  {
+  if constexpr (FEW) {
+    const int r = min(lane, a.R - 1);
+    const int start = ld_global<int>(a.starts + r), next = ld_global<int>(a.starts + r + 1);
+    const int len = ld_global<int>(a.lens + r);
+    Request mine = request_of(a, per, scan_max(max(start, 0)), next, len);
+    if (lane >= a.R) mine.line = 0.0;
+    const double upto = scan_sum(mine.line * kv_heads);
+    total = read_lane(upto, 63);
+    if (wave == 0) {
+      sh.request[lane] = mine;
+      sh.first[lane] = lane < a.R ? upto - mine.line * kv_heads : total + 1.0;
+    }
+    __syncthreads();
+  } else {
     int top = 0;
     for (int r = r0; r < r1; ++r) top = max(top, ld_global<int>(a.starts + r));
     const int upto = scan_max(top);
@@ -235,7 +319,11 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
     __syncthreads();
     sh.top[tid] = top = before;
     double sum = 0.0;
-    for (int r = r0; r < r1; ++r) sum += request(r, top).line * kv_heads;
+    for (int r = r0; r < r1; ++r) {
+      top = max(top, ld_global<int>(a.starts + r));
+      sum += request_of(a, per, top, ld_global<int>(a.starts + r + 1), ld_global<int>(a.lens + r)).line *
+             kv_heads;
+    }
     const double all = scan_sum(sum);
     if (lane == 63) sh.wave_sum[wave] = all;
     __syncthreads();
@@ -251,57 +339,70 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
     total = uniform(total);
   }
   const double unit = (double)per * kTile;   // of a tile of tokens
-  const double stretch = uniform(fmax(quotient(total + g.groups - 1, g.groups), kLeast * unit));
+  const double stretch =
+      uniform(fmax(quotient(total + g.groups - 1, g.groups, g.over_groups), kLeast * unit));
+  const double over_stretch = inverse(stretch);
   const int w = blockIdx.x;
   const double begin = w * stretch, stop = fmin(begin + stretch, total);
   double pos = begin;
-  int buf = 0;
+  Record *record = reinterpret_cast<Record *>(a.ws) + w;
+  if (tid == 0) record->parts = 0;
 
   while (pos < stop) {
-    // The item at pos.
+    // The item at pos: request r, key/value head kvh, the tile0-th of those.
     Request q;
-    int r, kvh, tile0;   // tile0: the item's number among the request's of this head
-    double item0, item_end;
-    {
+    int r;
+    double from;   // the request's first place
+    if constexpr (FEW) {
+      r = __builtin_popcountll(__ballot(sh.first[lane] <= pos)) - 1;
+      q = sh.request[r];
+      from = sh.first[r];
+    } else {
       int at = 0;
 #pragma unroll
       for (int i = 0; i < kThreads; i += 64) at += __builtin_popcountll(__ballot(sh.first[i + lane] <= pos));
       at -= 1;
       int top = sh.top[at];
-      double from = sh.first[at];
+      from = sh.first[at];
       r = at * each;
       for (;;) {
-        q = request(r, top);
+        top = max(top, ld_global<int>(a.starts + r));
+        q = request_of(a, per, top, ld_global<int>(a.starts + r + 1), ld_global<int>(a.lens + r));
         const double next = from + q.line * kv_heads;
         if (pos < next || r + 1 >= min(at * each + each, a.R)) break;
         from = next;
         ++r;
       }
-      kvh = min((int)quotient(pos - from, q.line), kv_heads - 1);
+      r = __builtin_amdgcn_readfirstlane(r);
+    }
+    q.from = __builtin_amdgcn_readfirstlane(q.from);
+    q.n = __builtin_amdgcn_readfirstlane(q.n);
+    q.old = __builtin_amdgcn_readfirstlane(q.old);
+    const int rows = q.n * per;
+    int kvh = min((int)quotient(pos - from, q.line, inverse(q.line)), kv_heads - 1), tile0;
+    double item0, item_end;
+    {
       from += kvh * q.line;
       const double o = pos - from, b = q.lead + kRows / 2;
       auto before = [&](int j) { return j * q.lead + (double)(kRows / 2) * j * (j + 1.0); };
-      int j = (int)((sqrt(b * b + 2.0 * kRows * o) - b) / kRows);
+      // (Nearly: the loops behind it find the tile.)
+      int j = (int)((__builtin_amdgcn_sqrtf((float)(b * b + 2.0 * kRows * o)) - (float)b) * (1.0f / kRows));
       j = max(min(j, q.tiles - 1), 0);
       while (j > 0 && before(j) > o) --j;
       while (j + 1 < q.tiles && before(j + 1) <= o) ++j;
-      tile0 = j;
-      item0 = from + before(j);
-      item_end = item0 + q.lead + fmin((j + 1.0) * kRows, q.rows);
+      tile0 = __builtin_amdgcn_readfirstlane(j);
+      item0 = uniform(from + before(j));
+      item_end = uniform(item0 + q.lead + min((j + 1) * kRows, rows));
     }
-    r = __builtin_amdgcn_readfirstlane(r);
     kvh = __builtin_amdgcn_readfirstlane(kvh);
-    tile0 = __builtin_amdgcn_readfirstlane(tile0);
-    item0 = uniform(item0);
-    item_end = uniform(item_end);
-    const int from = __builtin_amdgcn_readfirstlane(q.from), old = __builtin_amdgcn_readfirstlane(q.old);
-    const int m0 = tile0 * kRows;
-    const int count = min(kRows, __builtin_amdgcn_readfirstlane(q.n) * per - m0);
+    const int old = q.old;
+    const int m0 = tile0 * kRows, count = min(kRows, rows - m0);
     const int len = min(max(old + (m0 + count - 1) / per + 1, 0), a.max_len);   // that the last row sees
     const int tiles = (len + kTile - 1) / kTile;
     // Tiles [first, end) of the item are this stretch's.
+    const double tile_at = item0 + (double)kFixed * per;   // the place of the first
     auto cut = [&](double at) {
-      return at <= item0 ? 0 : (int)fmin(quotient(at - item0, unit), (double)tiles);
+      return at <= tile_at ? 0 : (int)fmin(quotient(at - tile_at, unit, g.over_unit), (double)tiles);
     };
     const int first = __builtin_amdgcn_readfirstlane(cut(begin));
     const int end = __builtin_amdgcn_readfirstlane(item_end <= stop ? tiles : cut(stop));
@@ -310,64 +411,179 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
     pos = fmax(fmin(item_end, stop), here + 1.0);   // (item_end > here: the loop ends in any case)
     if (first == end && !(tiles == 0 && here == item0)) continue;
 
+    const int64_t head_off = (int64_t)kvh * a.c.head_stride * S::kBytes;
+    const uint8_t *kbase = reinterpret_cast<const uint8_t *>(a.c.k) + head_off;
+    const uint8_t *vbase = reinterpret_cast<const uint8_t *>(a.c.v) + head_off;
+    const int32_t *table = a.tables + (int64_t)r * a.max_pages;
+    const uint32_t page_bytes = (uint32_t)(a.c.page_stride * S::kBytes);
+    const uint32_t tok_bytes = (uint32_t)(a.c.token_stride * S::kBytes);
+    const int tok_mask = (1 << a.c.page_shift) - 1;
+    const uint32_t lane_off = (lane / S::kPieces) * tok_bytes + 16 * (lane % S::kPieces);
+    // Staging: the 16-byte piece of tokens st0, st0 + kPass, ... of its group's block.
+    const int gt = tid & 255, piece = gt % S::kPieces, st0 = gt / S::kPieces;
+    const bool stages = S::kPieces >= 8 || st0 < kBlock;
+    uint8_t *const kd = sh.kv + part * (Sh::kKeyBytes + Sh::kValueBytes);
+    uint8_t *const vd = kd + Sh::kKeyBytes;
+
+    // Pages: of 16 tokens each, for a batch of tiles; or (small pages) of token c of
+    // the group's next block.
+    constexpr int kSixteens = kTile / 16, kBatch = 64 / kSixteens;
+    int pg_lo = 0, pg_hi = 0;
+    u32x4 kr[S::kLoads], vr[S::kLoads];   // the keys of the block after the values'
+    uint64_t off[S::kLoads];         // of the block whose keys are loaded
+    uint32_t scale_at = 0;
+    float v_exp0 = 0.0f, v_exp1 = 0.0f;   // 8-bit caches: exponent above the largest value scale
+    uint32_t mask0 = 0, mask1 = 0, mask2 = 0;   // tokens that are there: of the block worked
+                                                // on, the next one, the one loaded last
+    float ks_next = 0.0f, vs_next = 0.0f;   // of the block whose keys are loaded
+    auto page_at = [&](int token) { return ld_global<int>(table + (min(token, len - 1) >> a.c.page_shift)); };
+    // The first ones, asked for ahead of the queries.
+    int asked = 0;
+    if (first < end) asked = page_at(first * kTile + (HALVES ? 16 * lane : part * kBlock + c));
+    auto load_pages = [&](int tile) {   // of the tile, and of those behind it
+      int lo, hi = 0;
+      if constexpr (HALVES) {   // (in LDS: a register for them is one too many)
+        if ((tile - first) % kBatch == 0)
+          sh.pages[wave][lane] = tile == first ? asked : page_at(tile * kTile + 16 * lane);
+        __builtin_amdgcn_wave_barrier();
+        const int n = kSixteens * ((tile - first) % kBatch) + 2 * part;
+        lo = sh.pages[wave][n];
+        hi = sh.pages[wave][n + 1];
+      } else {
+        lo = tile == first ? asked : page_at(tile * kTile + part * kBlock + c);
+      }
+      pg_lo = lo;
+      pg_hi = hi;
+    };
+    // The rows of the keys of a tile: where they are, and which are there.
+    auto load_keys = [&](int tile) {
+      const int j0 = tile * kTile + part * kBlock;
+      if constexpr (HALVES) {
+        uint32_t page[2];
+        mask2 = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t p = __builtin_amdgcn_readfirstlane(i ? pg_hi : pg_lo);
+          const bool ok = p < (uint32_t)a.c.pages;
+          page[i] = ok ? p : 0;
+          mask2 |= ok ? 0xffffu << (16 * i) : 0;
+        }
+        const int left = len - j0;
+        if (left < kBlock) mask2 &= left <= 0 ? 0u : (1u << left) - 1;
+        if constexpr (kI8)
+          scale_at = (((c < 16 ? page[0] : page[1]) * (uint32_t)kv_heads + kvh) << a.c.page_shift) +
+                     ((j0 + c) & tok_mask);
+#pragma unroll
+        for (int l = 0; l < S::kLoads; ++l) {
+          const int t = rw * S::kWaveTokens + l * S::kPass;   // the wave's first
+          off[l] = (uint64_t)page[(t >> 4) & 1] * page_bytes +
+                   (uint64_t)(uint32_t)((j0 + t) & tok_mask) * tok_bytes + lane_off;
+        }
+      } else {
+        const bool ok = j0 + c < len && (uint32_t)pg_lo < (uint32_t)a.c.pages;
+        mask2 = (uint32_t)__ballot(ok);
+        const uint32_t page = ok ? pg_lo : 0, tok = ok ? (j0 + c) & tok_mask : 0;
+        if constexpr (kI8)
+          scale_at = ((page * (uint32_t)kv_heads + kvh) << a.c.page_shift) + tok;
+#pragma unroll
+        for (int l = 0; l < S::kLoads; ++l) {
+          const int t = (st0 + l * S::kPass) & (kBlock - 1);
+          off[l] = (uint64_t)(uint32_t)__shfl((int)page, t) * page_bytes +
+                   (uint64_t)(uint32_t)__shfl((int)tok, t) * tok_bytes + 16 * piece;
+        }
+      }
+      if (stages)
+#pragma unroll
+        for (int l = 0; l < S::kLoads; ++l) kr[l] = ld_global<u32x4>(kbase + off[l]);
+      if constexpr (kI8) {
+        ks_next = ld_global<float>(a.c.k_scale + scale_at);
+        vs_next = ld_global<float>(a.c.v_scale + scale_at);
+      }
+    };
+    auto load_values = [&]() {   // of the block whose keys were loaded last
+      if (stages)
+#pragma unroll
+        for (int l = 0; l < S::kLoads; ++l) vr[l] = ld_global<u32x4>(vbase + off[l]);
+    };
+    // 8-bit caches: the scales of the block whose keys are loaded.
+    auto stage_scales = [&](int tile, uint32_t mask) {
+      if constexpr (kI8) {
+        const bool ok = (mask >> c) & 1;
+        const float ks = ok ? ks_next : 0.0f, vs = ok && fabsf(vs_next) < INFINITY ? vs_next : 0.0f;
+        v_exp1 = exponent_above(across32(vs));
+        if (h == 0) {
+          sh.scales[wave][tile & 1][0][c] = ks;
+          sh.scales[wave][tile & 1][1][c] = vs;
+        }
+      }
+    };
+    auto stage_keys = [&](int n) {   // the n-th of this thread's pieces
+      const int t = st0 + n * S::kPass;
+      uint8_t *at = kd + t * S::kKeyRow + (kI8 ? 32 : 16) * piece;
+      if (!stages) return;
+      if constexpr (kI8) {
+        *reinterpret_cast<f16x8 *>(at) = codes_f16(kr[n].x, kr[n].y);
+        *reinterpret_cast<f16x8 *>(at + 16) = codes_f16(kr[n].z, kr[n].w);
+      } else {
+        *reinterpret_cast<u32x4 *>(at) = kr[n];
+      }
+    };
+    // Tokens that are not there get values of zero, and values that are not finite
+    // become finite: a row that must not see them has probabilities of zero for them.
+    auto stage_values = [&](uint32_t mask, int n) {
+      const int t = st0 + n * S::kPass;
+      uint8_t *at = vd + t * S::kValueRow + (kI8 ? 32 : 16) * piece;
+      if (!stages) return;
+      const bool ok = (mask >> t) & 1;
+      u32x4 v = vr[n];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (!kI8) {
+          typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+          constexpr unsigned short kMost = DT == BITNET_KV_BF16 ? 0x7f7f : 0x7bff;
+          const u16x2 m = __builtin_elementwise_min(
+              __builtin_bit_cast(u16x2, v[e] & 0x7fff7fffu), u16x2{kMost, kMost});
+          v[e] = __builtin_bit_cast(uint32_t, m) | (v[e] & 0x80008000u);
+        }
+        v[e] = ok ? v[e] : 0u;
+      }
+      if constexpr (kI8) {
+        *reinterpret_cast<f16x8 *>(at) = codes_f16(v.x, v.y);
+        *reinterpret_cast<f16x8 *>(at + 16) = codes_f16(v.z, v.w);
+      } else {
+        *reinterpret_cast<u32x4 *>(at) = v;
+      }
+    };
+    // The values of `tile` and the keys of the next one into LDS, and their
+    // successors' loads.  (Behind the last tile it is that once more, and not looked
+    // at.)
+    auto staging = [&](int tile) {
+#pragma unroll
+      for (int n = 0; n < S::kLoads; ++n) stage_values(mask0, n);
+      load_values();
+#pragma unroll
+      for (int n = 0; n < S::kLoads; ++n) stage_keys(n);
+      stage_scales(tile + 1, mask1);
+      load_keys(min(tile + 2, end - 1));
+      load_pages(min(tile + 3, end - 1));
+    };
+
+
     // This lane's row.
-    const int in = wave * kCols + c, m = m0 + min(in, count - 1);
-    const bool live = in < count, active = wave * kCols < count;
+    const int in = rw * kCols + c, m = m0 + min(in, count - 1);
+    const bool live = in < count, active = rw * kCols < count;
     const int i = m / per, head = kvh * per + (m - i * per);
     const int limit = min(max(old + i + 1, 0), a.max_len);
     // What the wave's first and last rows see.
     const int limit_lo = __builtin_amdgcn_readlane(limit, 0);
     const int limit_hi = active ? __builtin_amdgcn_readlane(limit, 31) : 0;
-    const int item_lo = min(max(old + m0 / per + 1, 0), a.max_len);
-    const int64_t out_row = (int64_t)(from + i) * a.q_heads + head;
-
-    const int64_t head_off = (int64_t)kvh * a.c.head_stride * S::kBytes;
-    const uint8_t *kbase = reinterpret_cast<const uint8_t *>(a.c.k) + head_off;
-    const uint8_t *vbase = reinterpret_cast<const uint8_t *>(a.c.v) + head_off;
-    const int32_t *table = a.tables + (int64_t)r * a.max_pages;
-    const uint64_t page_bytes = (uint64_t)a.c.page_stride * S::kBytes;
-    const uint32_t tok_bytes = (uint32_t)(a.c.token_stride * S::kBytes);
-    const int tok_mask = (1 << a.c.page_shift) - 1;
-    // Staging: this thread's 16-byte piece of tokens st0, st0 + kPass, ...
-    const int piece = tid % S::kPieces, st0 = tid / S::kPieces;
-    const bool stages = st0 < kTile;
-
-    int pg = 0;                      // page of token c of the tile after the loaded one
-    u32x4 kr[S::kLoads], vr[S::kLoads];
-    uint32_t mask_next = 0;          // tokens of the loaded tile that are there
-    float ksc = 0.0f, vsc = 0.0f;
-    auto load_page = [&](int tile) {
-      const int j = min(tile * kTile + c, len - 1);
-      pg = ld_global<int>(table + (j >> a.c.page_shift));
-    };
-    auto load_rows = [&](int tile) {
-      const int j = tile * kTile + c;
-      const bool ok = j < len && (uint32_t)pg < (uint32_t)a.c.pages;
-      mask_next = (uint32_t)__ballot(ok);
-      const uint32_t page = ok ? pg : 0, tok = ok ? j & tok_mask : 0;
-      if constexpr (kI8) {
-        const uint32_t at = ((page * (uint32_t)kv_heads + kvh) << a.c.page_shift) + tok;
-        ksc = ld_global<float>(a.c.k_scale + at);
-        vsc = ld_global<float>(a.c.v_scale + at);
-      }
-#pragma unroll
-      for (int l = 0; l < S::kLoads; ++l) {
-        const int t = (st0 + l * S::kPass) & (kTile - 1);
-        const uint64_t off = (uint64_t)(uint32_t)__shfl((int)page, t) * page_bytes +
-                             (uint64_t)(uint32_t)__shfl((int)tok, t) * tok_bytes + 16 * piece;
-        if (stages) {
-          kr[l] = ld_global<u32x4>(kbase + off);
-          vr[l] = ld_global<u32x4>(vbase + off);
-        }
-      }
-    };
-
-    if (first < end) load_page(first);
     // Queries as terms.
-    V qt[kSteps][kTerms];
+    constexpr int kKept = S::kKept;
+    V qt[kSteps][kKept];
+    uint8_t *qlds = sh.q + wave * 64 * D + 16 * lane;   // of the last term, 1 KB a step
     float unscale = 1.0f;   // of the scores
     {
-      const float *src = a.q + (int64_t)(from + i) * a.q_stride + (int64_t)head * D;
+      const float *src = a.q + (int64_t)(q.from + i) * a.q_stride + (int64_t)head * D;
       f32x4 x[kSteps][2];
 #pragma unroll
       for (int f = 0; f < kSteps; ++f) {
@@ -375,269 +591,376 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
         x[f][1] = ld_global<f32x4>(src + 16 * f + 8 * h + 4);
       }
       if (first < end) {
-        load_rows(first);
-        load_page(first + 1);
+        load_pages(first);
+        load_keys(first);
+        load_pages(min(first + 1, end - 1));
+        load_values();
       }
-      float big = 0.0f;
-#pragma unroll
-      for (int f = 0; f < kSteps; ++f)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[f][e >> 2][e & 3] *= a.scale * kLog2e;
-          big = fmaxf(big, fabsf(x[f][e >> 2][e & 3]));
-        }
-      float up = 1.0f;
+      float up = a.scale * kLog2e;
       if constexpr (F::kHalf) {
-        const float p2 = pow2_above(max2(big));
+        float big = 0.0f;
+#pragma unroll
+        for (int f = 0; f < kSteps; ++f)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[f][e >> 2][e & 3]));
+        const float p2 = pow2_above(max2(big) * fabsf(up));
         unscale = p2 * 0x1p-14f;
-        up = pow2_inverse(p2) * 0x1p14f;
+        up *= pow2_inverse(p2) * 0x1p14f;   // (exact)
       }
 #pragma unroll
       for (int f = 0; f < kSteps; ++f) {
         float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[f][e >> 2][e & 3] * up;
-        F::split(y, qt[f]);
+        for (int e = 0; e < 8; ++e) {
+          y[e] = x[f][e >> 2][e & 3] * up;
+          asm("" : "+v"(y[e]));
+        }
+        V t[kTerms];
+        F::split(y, t);
+#pragma unroll
+        for (int p = 0; p < kKept; ++p) qt[f][p] = t[p];
+        if constexpr (kKept < kTerms) *reinterpret_cast<V *>(qlds + 1024 * f) = t[kKept];
       }
     }
 
-    float mx = -INFINITY, l = 0.0f;   // mx in units of 1 / unscale
+    float base = -INFINITY, l = 0.0f;   // of the exponents, without kUp
     f32x16 o[kBlocks];
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
       for (int e = 0; e < 16; ++e) o[b][e] = 0.0f;
-    float vmax = pow2_above(0.0f);    // 8-bit caches: o is in units of this
+    f32x16 s[1];                      // scores
+    V p[2][kTerms];                   // probabilities
 
-    for (int tile = first; tile < end; ++tile) {
-      const uint32_t mask = mask_next;
-      const bool edge = (tile + 1) * kTile > item_lo;   // not every row sees all of the tile
-      // The tile into LDS.  Tokens that are not there get values of zero; where
-      // not every row sees every token, values that are not finite do too, so
-      // that they reach no row that must not see them.
-      if (stages) {
-#pragma unroll
-        for (int n = 0; n < S::kLoads; ++n) {
-          const int t = st0 + n * S::kPass;
-          u32x4 v = vr[n];
-          if (mask != 0xffffffffu && !((mask >> t) & 1)) v = u32x4{0u, 0u, 0u, 0u};
-          if (!kI8 && edge)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              constexpr uint32_t kInf = DT == BITNET_KV_BF16 ? 0x7f80u : 0x7c00u;
-              if ((v[e] & kInf) == kInf) v[e] &= 0xffff0000u;
-              if ((v[e] >> 16 & kInf) == kInf) v[e] &= 0xffffu;
-            }
-          if constexpr (kI8) {
-            uint8_t *kd = sh.k[buf] + t * S::kRow + 32 * piece, *vd = sh.v[buf] + t * S::kRow + 32 * piece;
-            *reinterpret_cast<f16x8 *>(kd) = codes_f16(kr[n].x, kr[n].y);
-            *reinterpret_cast<f16x8 *>(kd + 16) = codes_f16(kr[n].z, kr[n].w);
-            *reinterpret_cast<f16x8 *>(vd) = codes_f16(v.x, v.y);
-            *reinterpret_cast<f16x8 *>(vd + 16) = codes_f16(v.z, v.w);
-          } else {
-            *reinterpret_cast<u32x4 *>(sh.k[buf] + t * S::kRow + 16 * piece) = kr[n];
-            *reinterpret_cast<u32x4 *>(sh.v[buf] + t * S::kRow + 16 * piece) = v;
-          }
-        }
+    // The products of a turn: the outputs' with the block's values, then the scores'
+    // with the next one's keys; the LDS reads stay kAhead operands in front.
+    constexpr int kValues = 2 * kBlocks, kAhead = kKept < kTerms ? 2 : 3;
+    V ring[kAhead + 1], qring[kKept < kTerms ? kAhead + 1 : 1];
+    auto fetch = [&](int n) {   // operand n: values, then keys
+      if (n < kValues) {
+        const int cc = lane & 15;
+        const uint8_t *at = vd + (4 * h + (cc >> 2)) * S::kValueRow + 32 * (lane >> 4 & 1) + 8 * (cc & 3) +
+                            16 * (n / kBlocks) * S::kValueRow + 64 * (n % kBlocks);
+        s16x4 t[2];
+        t[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((BITNET_LDS s16x4 *)at);
+        t[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((BITNET_LDS s16x4 *)(at + 8 * S::kValueRow));
+        ring[n % (kAhead + 1)] = __builtin_bit_cast(V, t);
+      } else if (n < kValues + kSteps) {
+        const int f = n - kValues;
+        ring[n % (kAhead + 1)] = *reinterpret_cast<const V *>(kd + c * S::kKeyRow + 32 * f + 16 * h);
+        if constexpr (kKept < kTerms)
+          qring[n % (kAhead + 1)] = *reinterpret_cast<const V *>(qlds + 1024 * f);
       }
-      const float ks_now = ksc, vs_now = vsc;
-      if (tile + 1 < end) {
-        load_rows(tile + 1);
-        load_page(tile + 2);
+    };
+    auto product = [&](int n) {
+      const V &x = ring[n % (kAhead + 1)];
+      if (n < kValues) {
+        f32x16 &y = o[n % kBlocks];
+#pragma unroll
+        for (int t = kTerms - 1; t >= 0; --t) y = F::mfma(x, p[n / kBlocks][t], y);
+      } else {
+        const int f = n - kValues;
+        if constexpr (kKept < kTerms) s[0] = F::mfma(x, qring[n % (kAhead + 1)], s[0]);
+#pragma unroll
+        for (int t = kKept - 1; t >= 0; --t) s[0] = F::mfma(x, qt[f][t], s[0]);
       }
-      __syncthreads();
-      const uint8_t *krows = sh.k[buf], *vrows = sh.v[buf];
-      buf ^= 1;
-      if (tile * kTile >= limit_hi) continue;   // the wave sees none of it
-
-      const bool all = mask == 0xffffffffu && (tile + 1) * kTile <= limit_lo;
-      float ks[16], vs[16], vkeep = 1.0f;
-      if constexpr (kI8) {
-        const bool ok = (mask >> c) & 1;
-        if (h == 0) {
-          sh.scales[wave][0][c] = ok ? ks_now : 0.0f;
-          sh.scales[wave][1][c] = ok && fabsf(vs_now) < INFINITY ? vs_now : 0.0f;
-        }
-        __builtin_amdgcn_wave_barrier();
+    };
+    // Operands [FROM, TO).
+    auto turn = [&](auto from_, auto to_) {
+      constexpr int kFrom = decltype(from_)::value, kTo = decltype(to_)::value;
+      if constexpr (kTo > kValues)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[0][e] = 0.0f;
+#pragma unroll
+      for (int n = kFrom; n < kFrom + kAhead; ++n) fetch(n);
+#pragma unroll
+      for (int n = kFrom; n < kTo; ++n) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (n + kAhead < kTo) fetch(n + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
+        product(n);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr std::integral_constant<int, 0> kBegin{};
+    constexpr std::integral_constant<int, kValues> kBetween{};
+    constexpr std::integral_constant<int, kValues + kSteps> kEnd{};
+    // From the scores of a tile to its probabilities.
+    auto probabilities = [&](int tile, uint32_t mask) {
+      const int t0 = tile * kTile + part * kBlock;   // the wave's first token
+      const bool all = mask == 0xffffffffu && t0 + kBlock <= limit_lo;
+      // Those of this lane's tokens that its row sees: bit 8 a + e for token 8 a + 4 h + e.
+      const int left = limit - t0;
+      const uint32_t seen = (mask & (left >= kBlock ? ~0u : left <= 0 ? 0u : (1u << left) - 1)) >> 4 * h;
+      // The scales of this lane's 16 tokens.
+      auto scales = [&](int which, float (&y)[16]) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const f32x4 ks4 = *reinterpret_cast<const f32x4 *>(&sh.scales[wave][0][8 * b + 4 * h]);
-          const f32x4 vs4 = *reinterpret_cast<const f32x4 *>(&sh.scales[wave][1][8 * b + 4 * h]);
+          const f32x4 y4 = *reinterpret_cast<const f32x4 *>(&sh.scales[wave][tile & 1][which][8 * b + 4 * h]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            ks[4 * b + e] = ks4[e];
-            vs[4 * b + e] = vs4[e];
-          }
+          for (int e = 0; e < 4; ++e) y[4 * b + e] = y4[e];
         }
-        __builtin_amdgcn_wave_barrier();
-        // Relative to the power of two above the largest that the row has seen.
-        float big = 0.0f;
+      };
+      // Exponent above the largest of the values' scales that the row sees.
+      float v_exp = 0.0f;
+      if constexpr (kI8) {
+        v_exp = v_exp0;
+        if (!all) {
+          float big = 0.0f, vs[16];
+          scales(1, vs);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (!all && tile * kTile + 8 * (e >> 2) + 4 * h + (e & 3) >= limit) vs[e] = 0.0f;
-          big = fmaxf(big, vs[e]);
+          for (int e = 0; e < 16; ++e)
+            big = fmaxf(big, seen >> (8 * (e >> 2) + (e & 3)) & 1 ? vs[e] : 0.0f);
+          v_exp = exponent_above(max2(big));
         }
-        const float v_new = fmaxf(vmax, pow2_above(max2(big)));
-        const float inv = pow2_inverse(v_new);
-        vkeep = vmax * inv;
-        vmax = v_new;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) vs[e] *= inv;
       }
-
-      f32x16 s[1];
+      f32x16 &x = s[0];
+      if constexpr (kI8) {
+        float ks[16];
+        scales(0, ks);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s[0][e] = 0.0f;
-#pragma unroll
-      for (int f = 0; f < kSteps; ++f) {
-        const V k = *reinterpret_cast<const V *>(krows + c * S::kRow + 32 * f + 16 * h);
-#pragma unroll
-        for (int p = kTerms - 1; p >= 0; --p) s[0] = F::mfma(k, qt[f][p], s[0]);
+        for (int e = 0; e < 16; ++e) x[e] *= ks[e];
       }
-      settle<D>(s);
-      float x[16];
+      if (!all) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = kI8 ? s[0][e] * ks[e] : s[0][e];
-      if (!all)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int t = 8 * (e >> 2) + 4 * h + (e & 3);
-          if (!((mask >> t) & 1) || tile * kTile + t >= limit) x[e] = -INFINITY;
-        }
+        for (int e = 0; e < 16; ++e)
+          if (!(seen >> (8 * (e >> 2) + (e & 3)) & 1)) x[e] = -INFINITY;
+      }
       float top = x[0];
 #pragma unroll
       for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
-      const float m_new = fmaxf(mx, max2(top));
-      const float base = m_new == -INFINITY ? 0.0f : m_new;
-      const float lkeep = exp2_fast((mx - base) * unscale);
-      const float keep = lkeep * vkeep;
-      mx = m_new;
+      top = max2(top) * unscale + v_exp;
+      if (__any(top > base + kSlack)) {
+        const float b_new = fmaxf(base, top);
+        const float keep = base == -INFINITY ? 0.0f : exp2_fast(base - b_new);
+        base = b_new;
+        l *= keep;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) o[b] *= keep;
+      }
+      // (What rounds off the base is the same factor for all that a row sums up.)
+      const float shift = kUp - (base == -INFINITY ? 0.0f : base);
       float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        x[e] = exp2_fast(__builtin_fmaf(x[e] - base, unscale, kUp));
+        x[e] = exp2_fast(__builtin_fmaf(x[e], unscale, shift));
         sum += x[e];
       }
-      l = l * lkeep + sum;   // not in units of vmax
-      if constexpr (kI8)
+      l += sum;
+      if constexpr (kI8) {
+        float vs[16];
+        __builtin_amdgcn_sched_barrier(0);   // (asked for earlier they take registers too many)
+        scales(1, vs);
+        // (A scale above that of all that the row sees goes with a probability of zero.)
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] *= vs[e];
-      if (__any(keep != 1.0f))
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) o[b] *= keep;
+      }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[8 * half + e];
-        V p[kTerms];
-        F::split(y, p);
+        for (int e = 0; e < 8; ++e) {
+          y[e] = x[8 * half + e];
+          if constexpr (kI8) asm("" : "+v"(y[e]));   // one rounding of the product for both terms
+        }
+        F::split(y, p[half]);
+      }
+    };
+
+    // The groups of waves take turns: while one has its products on the matrix
+    // cores, the other works out its probabilities; a barrier between the turns
+    // keeps them apart.
+    if (first < end) {
+      mask0 = mask2;
+      stage_scales(first, mask0);
+      v_exp0 = v_exp1;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          const int cc = lane & 15;
-          const uint8_t *at = vrows + (16 * half + 4 * h + (cc >> 2)) * S::kRow + 64 * b +
-                              32 * (lane >> 4 & 1) + 8 * (cc & 3);
-          s16x4 t[2];
-          t[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((BITNET_LDS s16x4 *)at);
-          t[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((BITNET_LDS s16x4 *)(at + 8 * S::kRow));
-          const V v = __builtin_bit_cast(V, t);
-#pragma unroll
-          for (int n = kTerms - 1; n >= 0; --n) o[b] = F::mfma(v, p[n], o[b]);
+      for (int n = 0; n < S::kLoads; ++n) stage_keys(n);
+      load_keys(min(first + 1, end - 1));
+      load_pages(min(first + 2, end - 1));
+      mask1 = mask2;
+      __syncthreads();
+      if (kSplit == 2 && part == 1) __syncthreads();
+      auto next_masks = [&]() {
+        mask0 = mask1;
+        mask1 = mask2;
+        v_exp0 = v_exp1;
+      };
+      if (first * kTile + part * kBlock < limit_hi) {
+        turn(kBetween, kEnd);
+        settle<D>(s);
+        int tile = first;
+        for (; tile + 1 < end; ++tile) {
+          __syncthreads();
+          staging(tile);
+          probabilities(tile, mask0);
+          next_masks();
+          __syncthreads();
+          turn(kBegin, kEnd);
+          settle<D>(s);
+          settle<D>(o);
+        }
+        __syncthreads();
+        staging(tile);
+        probabilities(tile, mask0);
+        __syncthreads();
+        turn(kBegin, kBetween);
+        settle<D>(o);
+      } else {   // rows that see nothing of it: the staging alone
+        for (int tile = first; tile < end; ++tile) {
+          __syncthreads();
+          staging(tile);
+          next_masks();
+          __syncthreads();
         }
       }
-      settle<D>(o);
+      if (kSplit == 2 && part == 0) __syncthreads();
     }
-    mx *= unscale;
     l = sum2(l);
-    if constexpr (kI8)
+    // The groups of waves join: of a pair each wave keeps half of the channels.
+    constexpr int kMine = S::kMine;   // channel blocks, from b0 on
+    const int b0 = part * kMine;
+    f32x16 y[kMine];
+    __syncthreads();   // all are done with the tiles
+    if constexpr (kSplit == 2) {
+      uint8_t *mine_x = sh.kv + wave * (kMine * 4096) + 16 * lane;
+      const uint8_t *other_x = sh.kv + (wave ^ kRowWaves) * (kMine * 4096) + 16 * lane;
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) o[b] *= vmax;
-
-    auto finish = [&]() {
-      if (!live) return;
-      float *out = a.out + out_row * D;
-      const float over = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
+      for (int b = 0; b < kMine; ++b)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          f32x4 y = {o[b][4 * e], o[b][4 * e + 1], o[b][4 * e + 2], o[b][4 * e + 3]};
-          st_global<f32x4>(out + 32 * b + 8 * e + 4 * h,
-                           l > 0.0f ? y * over : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+          const f32x16 &z = part ? o[b] : o[kMine + b];
+          *reinterpret_cast<f32x4 *>(mine_x + (4 * b + e) * 1024) =
+              f32x4{z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]};
         }
-      if (a.lse && h == 0) a.lse[out_row] = l > 0.0f ? (mx - kUp + __log2f(l)) * kLn2 : -INFINITY;
-    };
-    if (whole) {
-      finish();
-      continue;
+      if (h == 0) {
+        sh.stats[wave][0][c] = base;
+        sh.stats[wave][1][c] = l;
+      }
+      __syncthreads();
+      const float base2 = sh.stats[wave ^ kRowWaves][0][c], l2 = sh.stats[wave ^ kRowWaves][1][c];
+      const float top = fmaxf(base, base2), zero = top == -INFINITY ? 0.0f : top;
+      const float f1 = exp2_fast(base - zero), f2 = exp2_fast(base2 - zero);
+      base = top;
+      l = l * f1 + l2 * f2;
+#pragma unroll
+      for (int b = 0; b < kMine; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f32x4 z = *reinterpret_cast<const f32x4 *>(other_x + (4 * b + e) * 1024);
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            y[b][4 * e + d] = (part ? o[kMine + b] : o[b])[4 * e + d] * f1 + z[d] * f2;
+        }
+      // (The next item's first tile goes where this was.)
+      if (pos < stop) __syncthreads();
+    } else {
+#pragma unroll
+      for (int b = 0; b < kMine; ++b) y[b] = o[b];
     }
 
-    // The stretches that hold the item: of them w_first is the first with a tile.
-    const int w_end = (int)quotient(item_end - 1.0, stretch);
-    const int w_first = min((int)quotient(item0 + unit - 1.0, stretch), w_end);
-    const int w_last = min((int)quotient(item0 + tiles * unit - 1.0, stretch), w_end);
-    const int parts = __builtin_amdgcn_readfirstlane(w_last - w_first + 1);
-    const int w0 = __builtin_amdgcn_readfirstlane(w_first);
-    auto place_of = [&](int ww) { return 2 * ww + (item0 > ww * stretch ? 1 : 0); };
-    constexpr uint32_t kPartBytes = kRows * D * 4;
-    const __amdgpu_buffer_rsrc_t outs = make_rsrc(a.ws + g.outs_off, 2 * g.groups * kPartBytes);
-    uint64_t *stats = reinterpret_cast<uint64_t *>(a.ws + g.stats_off);
-    const uint32_t mine = (wave * kBlocks * 4 * 64 + lane) * 16;
-    if (active) {
-      const uint32_t at = place_of(w) * kPartBytes + mine;
+    if (whole) {
+      if (live) {
+        // (Without a token the sums are zeros.)
+        const int64_t row = (int64_t)(q.from + i) * a.q_heads + head;
+        const float over = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
+        for (int b = 0; b < kMine; ++b)
+          store_block(a.out + row * D + 32 * (b0 + b) + 4 * h, y[b], over);
+        if (a.lse && h == 0 && part == 0) a.lse[row] = row_lse(base - kUp, l);
+      }
+      continue;
+    }
+    // A part of an item: into the workspace, for the join.
+    const int place = 2 * w + (item0 > begin ? 1 : 0);
+    if (active) {
+      float *part_out = reinterpret_cast<float *>(a.ws + g.outs_off) + (int64_t)place * kRows * D +
+                        (rw * kBlocks + b0) * 1024 + 4 * lane;
+#pragma unroll
+      for (int b = 0; b < kMine; ++b)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          st_device(outs, at + (b * 4 + e) * 1024,
-                     f32x4{o[b][4 * e], o[b][4 * e + 1], o[b][4 * e + 2], o[b][4 * e + 3]});
-      if (h == 0)
-        __hip_atomic_store((BITNET_GLOBAL uint64_t *)&stats[place_of(w) * kRows + in],
-                           __builtin_bit_cast(uint64_t, f32x2{mx, l}), __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
+          st_global<f32x4>(part_out + (4 * b + e) * 256,
+                           f32x4{y[b][4 * e], y[b][4 * e + 1], y[b][4 * e + 2], y[b][4 * e + 3]});
+      if (h == 0 && part == 0)
+        st_global<f32x2>(a.ws + g.stats_off + ((int64_t)place * kRows + in) * 8, f32x2{base - kUp, l});
     }
-    // Each wave's stores have been acknowledged before the counter moves.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    uint32_t *ticket = reinterpret_cast<uint32_t *>(a.ws) + w0;
-    if (tid == 0) {
-      const uint32_t n = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      sh.last = n == (uint32_t)parts - 1;
-      if (sh.last) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (first == 0 && tid == 0) {
+      // The last stretch that holds a tile of the item.
+      const int w_end = (int)quotient(item_end - 1.0, stretch, over_stretch);
+      const int w_last = min((int)quotient(tile_at + tiles * unit - 1.0, stretch, over_stretch), w_end);
+      *record = Record{w_last - w + 1, place, q.from, m0, count, kvh, {0, 0}};
     }
-    __syncthreads();
-    if (!sh.last || !active) continue;
-    auto stat = [&](int p) {
-      return __builtin_bit_cast(
-          f32x2, (uint64_t)__hip_atomic_load((const BITNET_GLOBAL uint64_t *)&stats[place_of(w0 + p) * kRows + in],
-                                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-    };
-    float tm = -INFINITY;
-    for (int p = 0; p < parts; ++p) tm = fmaxf(tm, stat(p).x);
-    const float base = tm == -INFINITY ? 0.0f : tm;
-    l = 0.0f;
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[b][e] = 0.0f;
-    for (int p = 0; p < parts; ++p) {
-      const f32x2 st = stat(p);
-      const uint32_t at = place_of(w0 + p) * kPartBytes + mine;
-      f32x4 y[kBlocks][4];
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[b][e] = ld_device(outs, at + (b * 4 + e) * 1024);
-      const float f = exp2_fast(st.x - base);
-      l += st.y * f;
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[b][e] += y[b][e >> 2][e & 3] * f;
-    }
-    mx = tm;
-    finish();
   }
+}
+
+// Joins the parts of the items that are cut: workgroup (w, group of 32 rows) the
+// item that begins in stretch w, a wave each 32 channels.
+template <int D>
+__global__ void __launch_bounds__(D * 2) join_kernel(ChunkArgs a, ChunkGrid g) {
+  constexpr int kBlocks = D / 32, kJoined = 8;
+  const Record &in = reinterpret_cast<const Record *>(a.ws)[blockIdx.x];
+  const int parts = in.parts;
+  const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5, b = threadIdx.x >> 6;
+  const int group = blockIdx.y, at_row = group * kCols + c;
+  if (parts == 0 || group * kCols >= in.count) return;
+  const float *outs = reinterpret_cast<const float *>(a.ws + g.outs_off) +
+                      (group * kBlocks + b) * 1024 + 4 * lane;
+  const float *stats = reinterpret_cast<const float *>(a.ws + g.stats_off) + 2 * at_row;
+  float top = -INFINITY, sum = 0.0f;
+  f32x16 z;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) z[e] = 0.0f;
+  for (int p0 = 0; p0 < parts; p0 += kJoined) {
+    f32x2 st[kJoined];
+    f32x4 x[kJoined][4];
+#pragma unroll
+    for (int u = 0; u < kJoined; ++u) {
+      const int p = p0 + u;
+      st[u] = f32x2{-INFINITY, 0.0f};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[u][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (p < parts) {
+        const int64_t place = p == 0 ? in.place : 2 * (int)(blockIdx.x + p);
+        st[u] = ld_global<f32x2>(stats + place * kRows * 2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[u][e] = ld_global<f32x4>(outs + place * kRows * D + e * 256);
+      }
+    }
+    float t = top;
+#pragma unroll
+    for (int u = 0; u < kJoined; ++u) t = fmaxf(t, st[u].x);
+    const float zero = t == -INFINITY ? 0.0f : t, keep = exp2_fast(top - zero);
+    top = t;
+    sum *= keep;
+    z *= keep;
+#pragma unroll
+    for (int u = 0; u < kJoined; ++u) {
+      const float f = exp2_fast(st[u].x - zero);
+      sum += st[u].y * f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) z[e] += x[u][e >> 2][e & 3] * f;
+    }
+  }
+  if (at_row >= in.count) return;
+  const int m = in.m0 + at_row, i = m / g.per;
+  const int64_t row = (int64_t)(in.from + i) * a.q_heads + in.kvh * g.per + (m - i * g.per);
+  store_block(a.out + row * D + 32 * b + 4 * h, z, sum > 0.0f ? 1.0f / sum : 0.0f);
+  if (a.lse && b == 0 && h == 0) a.lse[row] = row_lse(top, sum);
+}
+
+template <int DT, int D>
+void chunk_requests(const ChunkArgs &a, const ChunkGrid &g, hipStream_t stream) {
+  const bool halves =
+      a.c.page_shift >= 4 && a.c.token_stride * Operand<DT>::kBytes < ((int64_t)1 << 27);
+  if (a.R <= 64 && halves)
+    chunk_kernel<DT, D, true, true><<<g.groups, threads_of(D), 0, stream>>>(a, g);
+  else if (halves)
+    chunk_kernel<DT, D, false, true><<<g.groups, threads_of(D), 0, stream>>>(a, g);
+  else
+    chunk_kernel<DT, D, false, false><<<g.groups, threads_of(D), 0, stream>>>(a, g);
+  if (g.groups > 1)   // (else nothing is cut)
+    join_kernel<D><<<dim3(g.groups, kRows / kCols), 2 * D, 0, stream>>>(a, g);
 }
 
 template <int DT>
@@ -648,12 +971,14 @@ void chunk_type(const ChunkArgs &a, int D, hipStream_t stream) {
   g.stats_off = (int64_t)p.stats;
   g.groups = p.groups;
   g.per = a.q_heads / a.c.kv_heads;
+  g.over_groups = 1.0 / g.groups;
+  g.over_unit = 1.0 / ((double)g.per * kBlock * split_of(D));
   if (D == 64)
-    chunk_kernel<DT, 64><<<p.groups, kThreads, 0, stream>>>(a, g);
+    chunk_requests<DT, 64>(a, g, stream);
   else if (D == 128)
-    chunk_kernel<DT, 128><<<p.groups, kThreads, 0, stream>>>(a, g);
+    chunk_requests<DT, 128>(a, g, stream);
   else
-    chunk_kernel<DT, 256><<<p.groups, kThreads, 0, stream>>>(a, g);
+    chunk_requests<DT, 256>(a, g, stream);
 }
 
 }  // namespace

@@ -22,12 +22,14 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 // policy sc1), so that no workgroup has to write back or invalidate a cache,
 // as a fence of device scope does.
 constexpr int kDeviceAux = 16;
-__device__ __forceinline__ void st_device(__amdgpu_buffer_rsrc_t rsrc, uint32_t off, f32x4 v) {
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, off, 0, kDeviceAux);
+__device__ __forceinline__ void st_device(__amdgpu_buffer_rsrc_t rsrc, uint32_t off, f32x4 v,
+                                          uint32_t base = 0) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, off, base, kDeviceAux);
 }
-__device__ __forceinline__ f32x4 ld_device(__amdgpu_buffer_rsrc_t rsrc, uint32_t off) {
+__device__ __forceinline__ f32x4 ld_device(__amdgpu_buffer_rsrc_t rsrc, uint32_t off,
+                                           uint32_t base = 0) {
   return __builtin_bit_cast(f32x4,
-                            __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, kDeviceAux));
+                            __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, base, kDeviceAux));
 }
 
 // x as the sum of three bf16 terms (8 bits each), the largest first.
@@ -57,6 +59,24 @@ __device__ __forceinline__ void terms_f16(const float (&x)[8], f16x8 (&u)[2]) {
     asm("" : "+v"(y));
     u[0][e] = (_Float16)y;
     u[1][e] = (_Float16)(y - (float)u[0][e]);
+  }
+}
+
+// The same in packed conversions: four operations for two values.  The difference
+// is one fma of the fp16 half; x holds no product's result that is still exact.
+__device__ __forceinline__ void terms_f16_packed(const float (&x)[8], f16x8 (&u)[2]) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const f32x2 y = {x[e], x[e + 1]};
+    const f16x2 a = __builtin_convertvector(y, f16x2);
+    f32x2 r;
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r.x) : "v"(a), "v"(y.x));
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r.y) : "v"(a), "v"(y.y));
+    const f16x2 b = __builtin_convertvector(r, f16x2);
+    u[0][e] = a.x;
+    u[0][e + 1] = a.y;
+    u[1][e] = b.x;
+    u[1][e + 1] = b.y;
   }
 }
 

@@ -7,7 +7,10 @@ S = max_j scale * sum_i |q_i k_ji| and n tokens,
     |out - exact| <= u (2 (D + 16) S + 2 n + 64) sum_j p_j |v_j| + n LOST max |v|,
     |lse - exact| <= u ((D + 16) S + n + 64) + n LOST + u |lse|,
 LOST what a probability (relative to the largest) loses below its format's
-smallest numbers; lse is rounded once, and what its logarithm (2 u in units of
+smallest numbers: 2^-126 for bf16; fp16 terms are sums down to 2^-24, half of which
+is lost, of probabilities that are scaled to 2^9 or more at the largest, so 2^-34;
+with 8-bit values a token's scale relative to a power of two at most twice the
+largest one comes with it, so 2^-33.  lse is rounded once, and what its logarithm (2 u in units of
 log 2, at most 24 of them) adds lies in the 64.
 
 Norm and gated activation: fp64, rounded once: |y - exact| <= (1/2 ulp) (1 +
@@ -24,9 +27,10 @@ import numpy as np
 import pytest
 
 from oracle import prompt as ref
-from tests.test_gpu_decode_step import LOST, U, dev, host, say, tb  # noqa: F401
+from tests.test_gpu_decode_step import U, dev, host, say, tb  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+LOST = {"bf16": 2.0 ** -126, "fp16": 2.0 ** -34, "int8": 2.0 ** -33}
 
 
 # ---- chunk attention ------------------------------------------------------------
@@ -114,12 +118,10 @@ def run_chunk(tb, pg, q, starts, lens, H, scale=None, max_len=None, pad=8, strid
     n = tb.bitnet_chunk_attention_workspace_bytes(T, R, H, pg.KV, D, max_len)
     if ws is None:
         ws = torch.full((n + 256,), 0xAB, dtype=torch.uint8, device="cuda:0")
-        ws[:tb.CHUNK_COUNTERS].zero_()
     i32 = lambda a: dev(np.asarray(a, np.int64).astype(np.int32))
     for _ in range(2):   # the second call finds what the first left
         tb.bitnet_chunk_attention_into(pg.cache, pg.layer, T, H, qd, i32(starts), i32(lens),
                                        i32(pg.tables), max_len, scale, out, ws[:n], lse)
-        assert (ws[:tb.CHUNK_COUNTERS] == 0).all().item(), "counters"
     assert (ws[n:] == 0xAB).all().item(), "behind the workspace"
     o, l = host(out), host(lse)
     assert (o[T:] == -77).all() and (l[T:] == -77).all(), "behind the outputs"
@@ -299,7 +301,6 @@ def test_chunk_one_workspace_for_all_shapes(tb):
     import torch
     rng = np.random.default_rng(9)
     ws = torch.full((80 << 20,), 0xAB, dtype=torch.uint8, device="cuda:0")
-    ws[:tb.CHUNK_COUNTERS].zero_()
     for dtype, D, new, old in (("bf16", 128, [4], [800]), ("int8", 64, [90, 2], [0, 400]),
                                ("fp16", 256, [20], [600]), ("fp16", 128, [300], [0])):
         say(f"[chunk] shared workspace {dtype} {D}")
