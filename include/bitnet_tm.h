@@ -780,7 +780,7 @@ bitnet_status bitnet_beam_reorder(const bitnet_kv_cache *cache, int64_t B, int64
  *   sum_out (optional) takes h; it may be residual or x itself where their
  *   rows are contiguous.
  * bitnet_silu_mul: y = fl32(gate * up / (1 + exp(-gate))), in the same way
- *   (2^-48); y may be gate or up itself where their rows are contiguous.
+ *   (2^-44); y may be gate or up itself where their rows are contiguous.
  *
  * x, residual, gate and up are fp32 rows of K values, their rows x_stride, ...
  * elements apart; weight fp32 [K]; y, sum_out fp32 and xq int8 [M][K]
