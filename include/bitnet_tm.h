@@ -673,10 +673,12 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
  *   last of the lens[r] tokens that request r holds in the pages of table row
  *   r; the i-th of them attends to the first lens[r] - n + i + 1:
  *     out[t][h] = sum_j p_j v_j,  p = softmax_j(scale * q[t][h] . k_j),
- *   heads, lse, precision and what has to be finite as bitnet_paged_attention
- *   (which it equals within both calls' errors), except that an 8-bit value
- *   whose scale is not finite counts as zero.  A token has no influence on rows
- *   that come before it, whatever it holds.
+ *   heads, lse and what has to be finite as for bitnet_paged_attention (which it
+ *   equals within both calls' errors), and the precision too, except that with
+ *   fp16 and int8 caches what lies below 2^-33 of the largest probability (times
+ *   the largest value scale) may count as zero, and that an 8-bit row whose value
+ *   scale is not finite does.  A token has no influence on rows that come before
+ *   it, whatever it holds.
  *   starts int32 [R+1] (bitnet_kv_map's) and lens int32 [R] (its state's first
  *   entries) are device data.  Starts are taken in ascending order (each as
  *   the largest up to it) and clamped to [0, T], lengths to [0, max_len].  A
@@ -686,8 +688,10 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
  *   tables int32 [R][max_pages]; pages out of range, entries and slots behind
  *   the length as for bitnet_paged_attention.
  *   1 <= R <= BITNET_MAX_ROWS; T, heads, max_len, strides and alignment as for
- *   bitnet_paged_attention.  T == 0 launches nothing.  out, lse and workspace
- *   must overlap neither each other, nor the inputs, nor the layer.
+ *   bitnet_paged_attention, and with g = q_heads / kv_heads
+ *   kv_heads * (T*g/128 + R) * (max_len + 512) * g below 2^52.  T == 0 launches
+ *   nothing.  out, lse and workspace must overlap neither each other, nor the
+ *   inputs, nor the layer.
  *   workspace: bitnet_chunk_attention_workspace_bytes(...) bytes, 256-byte
  *   aligned; what it holds before does not matter, and nothing is kept in it
  *   from one call to the next (calls that share it must not overlap in time).

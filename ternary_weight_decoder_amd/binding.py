@@ -765,7 +765,10 @@ def bitnet_kv_map_into(pool: KvPool, T, new_lens, state_in, state_out, starts, s
 
 def _rows_stride(t, width):
     """Elements between the rows of a [T, width] tensor with contiguous rows."""
-    return t.stride(0) if t.size(0) > 1 else max(width, 4)
+    s = t.stride(0)
+    if width <= s < 1 << 31 and not s & 3:   # (the usual case, without asking for T)
+        return s
+    return s if t.size(0) > 1 else max(width, 4)
 
 
 def bitnet_kv_append_into(cache: KvCache, layer, T, q_heads, k, v, slots, positions=None, cos=None,

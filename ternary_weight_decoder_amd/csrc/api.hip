@@ -1101,10 +1101,13 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
   return from_hip(launch_attend(a, cache->dtype, cache->head_dim, as_stream(stream)));
 }
 
-// Shapes of an attention call over chunks, apart from the cache's own.
+// Shapes of an attention call over chunks, apart from the cache's own.  The kernel
+// counts its work in whole numbers held in fp64.
 static bool chunk_shape_ok(int64_t T, int64_t R, int64_t q_heads, int64_t kv_heads, int64_t D,
                            int64_t max_len) {
-  return attend_shape_ok(T, q_heads, kv_heads, D, max_len) && R >= 1 && R <= kMaxRows;
+  if (!attend_shape_ok(T, q_heads, kv_heads, D, max_len) || R < 1 || R > kMaxRows) return false;
+  const int64_t per = q_heads / kv_heads, items = kv_heads * (T * per / 128 + R);
+  return (__int128)items * (max_len + 512) * per < ((__int128)1 << 52);
 }
 
 size_t bitnet_chunk_attention_workspace_bytes(int64_t T, int64_t R, int64_t q_heads,
