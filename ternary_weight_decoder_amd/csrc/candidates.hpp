@@ -78,6 +78,7 @@ struct CandidateShared {
   __attribute__((aligned(16))) u64 cand[kWords];   // the waves' lists, then candidates
   u64 best[MAXW];                      // the W largest keys, in order
   u64 bound[kWaves];
+  uint32_t share[kWaves];
   float m[kWaves], s[kWaves];
   uint32_t count, last;
 };
@@ -161,14 +162,31 @@ __device__ __forceinline__ u64 wave_bound(u64 key, int W, int most) {
 // the workgroup in step, and has its keys in registers.
 template <int N, int MAXW, int WORDS, typename Key>
 __device__ __forceinline__ void select_largest(CandidateShared<MAXW, WORDS> &sh, int W, u64 mine, Key key) {
+  // What every wave reaches with its share of W lanes is a bound too, below which are
+  // most of the keys that reach a wave's own for all W: the ranking reads the square
+  // of what is left (32 of a row of 151,936: 26.8 us without, 14.5 with; 20: 13.0 and
+  // 12.2).
+  constexpr bool kShares = MAXW > 8;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const u64 b = wave_bound(mine, W, MAXW);
   if (lane == 0) sh.bound[wave] = b;
+  if constexpr (kShares) {
+    const int n = (W + kWaves - 1) / kWaves;
+    int at;
+    const uint32_t share = bound_32((uint32_t)(mine >> 32), n, n + 2, &at);
+    if (lane == 0) sh.share[wave] = share;
+  }
   if (tid == 0) sh.count = 0;
   __syncthreads();
   u64 bound = 1;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) bound = sh.bound[w] > bound ? sh.bound[w] : bound;
+  if constexpr (kShares) {
+    uint32_t least = sh.share[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) least = min(least, sh.share[w]);
+    bound = max(bound, (u64)least << 32);
+  }
   if (mine >= bound)
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -177,12 +195,15 @@ __device__ __forceinline__ void select_largest(CandidateShared<MAXW, WORDS> &sh,
     }
   __syncthreads();
   const int all = sh.count;
-  for (int i = tid; i < all; i += kThreads) {
+  // Four threads count for each (one: 20 of a row 0.5 us more).
+  for (int i = tid >> 2; i < all; i += kThreads / 4) {
     const u64 k = sh.cand[i];
     int r = 0;
 #pragma unroll 4
-    for (int c = 0; c < all; ++c) r += sh.cand[c] > k ? 1 : 0;
-    if (r < W) sh.best[r] = k;
+    for (int c = tid & 3; c < all; c += 4) r += sh.cand[c] > k ? 1 : 0;
+    r += __builtin_amdgcn_update_dpp(0, r, 0xB1, 0xF, 0xF, false);
+    r += __builtin_amdgcn_update_dpp(0, r, 0x4E, 0xF, 0xF, false);
+    if (r < W && (tid & 3) == 0) sh.best[r] = k;
   }
   if (tid >= all && tid < W) sh.best[tid] = 0;
   __syncthreads();

@@ -528,6 +528,26 @@ def test_logprobs_edges(tb):
             check_logprobs(tb, x, tokens, top)
 
 
+@pytest.mark.parametrize("V,top", [(4096, 32), (4001, 20), (9000, 8), (151936, 32), (70000, 9)])
+def test_logprobs_orders(tb, V, top):
+    """Rows whose largest lie together: sorted both ways, in one thread's quads, in one
+    wave's, in the last chunk, all the same, two values, a few above many equal ones."""
+    rng = np.random.default_rng(V + top)
+    up = np.arange(V, dtype=np.float32) / V
+    one = rng.normal(0, 1, V).astype(np.float32)
+    one[4:8] += 20
+    one[1028:1032] += 20
+    wave = rng.normal(0, 1, V).astype(np.float32)
+    wave[256:512] += 20
+    last = rng.normal(0, 1, V).astype(np.float32)
+    last[-40:] += 20
+    few = np.full(V, -3.0, np.float32)
+    few[rng.choice(V, top // 2, replace=False)] = 1.0
+    x = np.stack([up, up[::-1], one, wave, last, np.full(V, 2.5, np.float32),
+                  rng.integers(0, 2, V).astype(np.float32), few])
+    check_logprobs(tb, x, rng.integers(0, V, len(x)).astype(np.int32), top)
+
+
 def test_logprobs_nothing_left_of_a_row_adds_nothing_elsewhere(tb):
     """Outputs that are not asked for are not written, and a row's results do not
     depend on the others'."""
