@@ -6,8 +6,17 @@
 //
 // A key/value row serves all new tokens of its request and all query heads of
 // its group, so the rows of the product are (token, head) pairs, 128 of them to
-// an item, a wave each 32; tiles of 32 tokens of keys and values go through LDS
-// once for the item.  The work is bound by the matrix cores.
+// an item, 32 to a wave.  The work is bound by the matrix cores where it is long,
+// and by what each item has to wait for where it is short.
+//
+// Groups.  An item has two groups of four waves (a SIMD's two waves are one of
+// each), a block of 32 tokens of the 64-token tile each, in LDS of its own.  They
+// take turns: one has its products on the matrix cores (the values of its block,
+// then the keys of its next one) while the other goes from scores to
+// probabilities and stages what was loaded; a barrier lies between the turns.
+// (Eight waves that each do both by themselves: 1800 fp16 tokens 60 us, in turns 46.)
+// In the end the groups join in LDS.  With 256 channels a wave's outputs and
+// queries fill the registers of its SIMD alone, and there is one group.
 //
 // Tile.  Keys are the row operand of v_mfma_f32_32x32x16 and queries the column
 // operand, so the scores arrive transposed: lane (c, h) holds column c, tokens
@@ -27,9 +36,19 @@
 // line, which is cut into equal stretches, a workgroup each, from the lengths
 // on the device.  A tile of an item costs what its last row sees, counted in
 // rows: a linear function of the tile's number, so every place on the line has
-// a closed form and no list of items is made.  A stretch may hold the end of an
-// item, whole ones and the beginning of another; the parts of an item are joined
-// by the workgroup that finishes last.
+// a closed form and no list of items is made.  What an item's beginning and end
+// cost (queries as terms, the first tiles' way from memory, the joining) counts as
+// kFixed tokens.  A stretch may hold the end of an item, whole ones and the
+// beginning of another; the parts of items that are cut go to the workspace, and a
+// second launch joins them.  (Its launch takes 2 us and what it reads and writes 2
+// of a tail of 4 tokens, 6 of a prompt of 1800, near HBM's rate.)
+//
+// Measured, 12 heads over 2 of 128 channels: 1800 fp16 tokens 44 us (20 GFLOP of
+// terms' products: 18 us at a large product's rate; then 2 us of start, 3 of plan
+// and place, 6 of first tiles and queries for each of an item's parts, 8 of parts and
+// join); 16 requests of 1..256 tokens behind up to 1800 in 8 bits 63 us; 450 bf16
+// tokens behind 32,317 233 to 250 us by the card (270 GFLOP: 1.08 to 1.16 PFLOP/s, a
+// large product's rate); 4 tokens behind 253 14.5 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -54,9 +73,13 @@ constexpr int threads_of(int D) { return 64 * kRowWaves * split_of(D); }
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-constexpr int kGrid = 256;                // workgroups: one a compute unit
-constexpr int kFixed = 256;               // tokens that an item's beginning and end cost as much as
-constexpr int kLeast = 1;                 // tiles of a stretch, at least
+// Workgroups, one a compute unit (512: the prompt of 1800 tokens 58 us, 48 with 256).
+constexpr int kGrid = 256;
+// Tokens that an item's beginning and end cost as much as (96, 192, 256, 384: that
+// prompt 58, 49.6, 46.4, 45.1 us, 16 ragged requests 75, 63.4, 63.7, 65.3).
+constexpr int kFixed = 256;
+// Tiles of a stretch, at least (1, 2, 4: a tail of 4 tokens 15.1, 14.6, 17.0 us).
+constexpr int kLeast = 2;
 
 struct ChunkPlan {
   int groups;
@@ -265,8 +288,10 @@ __device__ __forceinline__ float row_lse(float base, float sum) {
   return sum > 0.0f ? (base + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
-// FEW: up to 64 requests, which every wave holds a lane each.
-// HALVES: 16 tokens in a row always lie on one page, at 32-bit offsets.
+// FEW: up to 64 requests, which every wave holds a lane each (through LDS instead, as
+// for more: a prompt 1 us more, 450 tokens at 32,767 6 us).
+// HALVES: 16 tokens in a row always lie on one page, at 32-bit offsets (a page a token
+// instead: a prompt 2 us more, 8-bit requests the same).
 template <int DT, int D, bool FEW, bool HALVES>
 __global__ void __launch_bounds__(threads_of(D)) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
 chunk_kernel(ChunkArgs a, ChunkGrid g) {
