@@ -179,11 +179,13 @@ __global__ void __launch_bounds__(64 * WAVES) gate_kernel(GateArgs a) {
   if (a.xq) store_codes<WAVES, VEC>(y, t, quads, a.xq + row * a.K, a.x_scale + row, sh);
 }
 
-// fp32 rows alone: no row has to be held, a quad a thread.
+// fp32 rows alone: no row has to be held, a quad a thread, as many threads a row as it
+// has quads, up to 256 (always 256: 100,000 rows of 64 34 us, 13 so).
 __global__ void __launch_bounds__(256) gate_flat_kernel(GateArgs a) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= a.K >> 2) return;
-  for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
+  for (int64_t row = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; row < a.M;
+       row += (int64_t)gridDim.y * blockDim.y) {
     const f32x4 g = ld_global<f32x4>(a.gate + row * a.g_stride + 4 * i);
     const f32x4 u = ld_global<f32x4>(a.up + row * a.u_stride + 4 * i);
     f32x4 y;
@@ -201,12 +203,18 @@ dim3 row_grid(int64_t blocks) {
 }  // namespace
 
 // A row's values are held by as few waves as their registers allow at full
-// occupancy: 4 waves with 2 quads a lane up to 2048 values, 8 with 5 up to 10240, 16
-// with 8 beyond.  (1800 rows of 1536: 8.8 us, 10.6 with a wave a row and 6 quads a
-// lane; 16 of them 2.7 against 4.3.  1800 gated rows of 8960: 33.3 us, 35 with 4
-// waves and 9 quads, 40 with 16 waves and 3.)
+// occupancy: 1, 2 and 4 waves with 2 quads a lane up to 512, 1024 and 2048 values, 8
+// with 5 up to 10240, 16 with 8 beyond.  (1800 rows of 1536: 8.8 us, 10.6 with a wave a
+// row and 6 quads a lane; 16 of them 2.7 against 4.3.  1800 gated rows of 8960: 33.3
+// us, 35 with 4 waves and 9 quads, 40 with 16 waves and 3.  With 4 waves a row 16,571
+// rows of 100 take 24.7 us, 9.3 with one; 30,000 gated rows of 1000 in 8 bits 64, 41
+// with two.)
 hipError_t launch_add_rms_norm(const NormArgs &a, hipStream_t stream) {
-  if (a.K <= 2048)
+  if (a.K <= 512)
+    norm_kernel<1, 2><<<row_grid(a.M), 64, 0, stream>>>(a);
+  else if (a.K <= 1024)
+    norm_kernel<2, 2><<<row_grid(a.M), 128, 0, stream>>>(a);
+  else if (a.K <= 2048)
     norm_kernel<4, 2><<<row_grid(a.M), 256, 0, stream>>>(a);
   else if (a.K <= 10240)
     norm_kernel<8, 5><<<row_grid(a.M), 512, 0, stream>>>(a);
@@ -216,8 +224,17 @@ hipError_t launch_add_rms_norm(const NormArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_silu_mul(const GateArgs &a, hipStream_t stream) {
+  const int quads = a.K / 4;
+  int across = 1;
+  while (across < quads && across < 256) across *= 2;
+  const int rows = 256 / across;
   if (!a.xq)
-    gate_flat_kernel<<<dim3((a.K / 4 + 255) / 256, std::min(a.M, 65535)), 256, 0, stream>>>(a);
+    gate_flat_kernel<<<dim3((quads + across - 1) / across, std::min((a.M + rows - 1) / rows, 65535)),
+                       dim3(across, rows), 0, stream>>>(a);
+  else if (a.K <= 512)
+    gate_kernel<1, 2><<<row_grid(a.M), 64, 0, stream>>>(a);
+  else if (a.K <= 1024)
+    gate_kernel<2, 2><<<row_grid(a.M), 128, 0, stream>>>(a);
   else if (a.K <= 2048)
     gate_kernel<4, 2><<<row_grid(a.M), 256, 0, stream>>>(a);
   else if (a.K <= 10240)

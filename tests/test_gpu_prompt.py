@@ -320,7 +320,8 @@ def near(got, want):
 
 
 ROW_SIZES = [(1, 4), (1, 1536), (3, 64), (16, 1536), (5, 100), (17, 2048), (7, 2052), (16, 8960),
-             (3, 10240), (2, 10244), (1, 32768), (1030, 1536), (1025, 260), (33, 8960), (260, 2056)]
+             (3, 10240), (2, 10244), (1, 32768), (1030, 1536), (1025, 260), (33, 8960), (260, 2056),
+             (2000, 8), (700, 12), (300, 512), (257, 516), (99, 1024), (65, 1028), (9, 256), (5, 252)]
 
 
 def outliers(rng, M, K):
