@@ -85,10 +85,11 @@ struct ChunkPlan {
   int groups;
   size_t outs, stats, total;   // workspace offsets; records first
 };
-// Of a workgroup: the item whose first part it has.  Its parts' places are `place`,
-// then every second one from 2 (w + 1) on.
+// Of a place in the workspace, of which a workgroup has two: the item of which it holds
+// a part (parts: 0 for none).  The parts' places are `place`, then every second one from
+// 2 (w + 1) on.
 struct Record {
-  int32_t parts, place, from, m0, count, kvh, pad[2];
+  int32_t parts, w, place, from, m0, count, kvh, pad;
 };
 
 ChunkPlan chunk_plan(int64_t T, int64_t R, int64_t q_heads, int64_t kv_heads, int64_t D,
@@ -99,7 +100,7 @@ ChunkPlan chunk_plan(int64_t T, int64_t R, int64_t q_heads, int64_t kv_heads, in
   p.groups = (int)std::min<int64_t>(kGrid, items * (tiles + kFixed / tile));
   // Two places a workgroup: for the item at its beginning and the one at its end.
   const size_t rows = 2 * (size_t)p.groups * kRows;
-  p.outs = kGrid * sizeof(Record);
+  p.outs = 2 * kGrid * sizeof(Record);
   p.stats = p.outs + rows * D * 4;
   p.total = p.stats + rows * 8;
   return p;
@@ -370,8 +371,8 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
   const int w = blockIdx.x;
   const double begin = w * stretch, stop = fmin(begin + stretch, total);
   double pos = begin;
-  Record *record = reinterpret_cast<Record *>(a.ws) + w;
-  if (tid == 0) record->parts = 0;
+  Record *records = reinterpret_cast<Record *>(a.ws);
+  if (tid < 2) records[2 * w + tid].parts = 0;
 
   while (pos < stop) {
     // The item at pos: request r, key/value head kvh, the tile0-th of those.
@@ -910,68 +911,121 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
       if (h == 0 && part == 0)
         st_global<f32x2>(a.ws + g.stats_off + ((int64_t)place * kRows + in) * 8, f32x2{base - kUp, l});
     }
-    if (first == 0 && tid == 0) {
-      // The last stretch that holds a tile of the item.
+    if (tid == (place & 1)) {   // (which cleared it)
+      // The first and the last stretch that hold a tile of the item.
+      const int w0 = (int)quotient(tile_at + unit - 1.0, stretch, over_stretch);
       const int w_end = (int)quotient(item_end - 1.0, stretch, over_stretch);
       const int w_last = min((int)quotient(tile_at + tiles * unit - 1.0, stretch, over_stretch), w_end);
-      *record = Record{w_last - w + 1, place, q.from, m0, count, kvh, {0, 0}};
+      records[place] = Record{w_last - w0 + 1, w0, 2 * w0 + (item0 > w0 * stretch ? 1 : 0),
+                              q.from, m0, count, kvh, 0};
     }
   }
 }
 
-// Joins the parts of the items that are cut: workgroup (w, group of 32 rows) the
-// item that begins in stretch w, a wave each 32 channels.
+// Joins the parts of the items that are cut.  The workgroups of an item's n parts share
+// the work, kHelpers for each: blocks of 32 rows and 32 channels, a wave each; from
+// kMany parts on a quarter of the channels each, and a quarter of the parts to a wave.
+// (A workgroup for each item and 32 rows of it: 8 tokens at 12,324 of 8 bits take 37.5
+// us, 19.5 so, 64 at 32,064 63 and 21.7, a prompt of 512 23.4 and 24.1; kHelpers 1 and 4
+// and kMany 8 and 6 leave that prompt at 25 to 26.)
+constexpr int kHelpers = 2, kMany = 16;
+
 template <int D>
-__global__ void __launch_bounds__(D * 2) join_kernel(ChunkArgs a, ChunkGrid g) {
-  constexpr int kBlocks = D / 32, kJoined = 8;
-  const Record &in = reinterpret_cast<const Record *>(a.ws)[blockIdx.x];
-  const int parts = in.parts;
-  const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5, b = threadIdx.x >> 6;
-  const int group = blockIdx.y, at_row = group * kCols + c;
-  if (parts == 0 || group * kCols >= in.count) return;
-  const float *outs = reinterpret_cast<const float *>(a.ws + g.outs_off) +
-                      (group * kBlocks + b) * 1024 + 4 * lane;
-  const float *stats = reinterpret_cast<const float *>(a.ws + g.stats_off) + 2 * at_row;
-  float top = -INFINITY, sum = 0.0f;
-  f32x16 z;
+__global__ void __launch_bounds__(256) join_kernel(ChunkArgs a, ChunkGrid g) {
+  constexpr int kBlocks = D / 32;
+  __shared__ f32x4 sh_z[4][64];
+  __shared__ f32x2 sh_st[4][64];
+  const Record in = reinterpret_cast<const Record *>(a.ws)[blockIdx.x];
+  if (in.parts == 0) return;
+  const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int helper = ((int)(blockIdx.x >> 1) - in.w) * kHelpers + blockIdx.y, helpers = in.parts * kHelpers;
+  const int blocks = (in.count + kCols - 1) / kCols * kBlocks;
+  const float *outs = reinterpret_cast<const float *>(a.ws + g.outs_off) + 4 * lane;
+  const float *stats = reinterpret_cast<const float *>(a.ws + g.stats_off) + 2 * c;
+  // Adds up to J parts first, first + step, ... of block `at`, E quads of a lane from e0 on.
+  auto add = [&](auto J_, int at, int e0, int first, int step, float &top, float &sum, auto &z) {
+    constexpr int J = decltype(J_)::value, E = sizeof(z) / sizeof(z[0]);
+    f32x2 st[J];
+    f32x4 x[J][E];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) z[e] = 0.0f;
-  for (int p0 = 0; p0 < parts; p0 += kJoined) {
-    f32x2 st[kJoined];
-    f32x4 x[kJoined][4];
-#pragma unroll
-    for (int u = 0; u < kJoined; ++u) {
-      const int p = p0 + u;
+    for (int u = 0; u < J; ++u) {
+      const int p = first + u * step;
       st[u] = f32x2{-INFINITY, 0.0f};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[u][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (p < parts) {
-        const int64_t place = p == 0 ? in.place : 2 * (int)(blockIdx.x + p);
-        st[u] = ld_global<f32x2>(stats + place * kRows * 2);
+      for (int e = 0; e < E; ++e) x[u][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (p < in.parts) {
+        const int64_t place = p == 0 ? in.place : 2 * (in.w + p);
+        st[u] = ld_global<f32x2>(stats + (place * kRows + at / kBlocks * kCols) * 2);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[u][e] = ld_global<f32x4>(outs + place * kRows * D + e * 256);
+        for (int e = 0; e < E; ++e)
+          x[u][e] = ld_global<f32x4>(outs + place * kRows * D + at * 1024 + (e0 + e) * 256);
       }
     }
     float t = top;
 #pragma unroll
-    for (int u = 0; u < kJoined; ++u) t = fmaxf(t, st[u].x);
+    for (int u = 0; u < J; ++u) t = fmaxf(t, st[u].x);
     const float zero = t == -INFINITY ? 0.0f : t, keep = exp2_fast(top - zero);
     top = t;
     sum *= keep;
-    z *= keep;
 #pragma unroll
-    for (int u = 0; u < kJoined; ++u) {
+    for (int e = 0; e < E; ++e) z[e] *= keep;
+#pragma unroll
+    for (int u = 0; u < J; ++u) {
       const float f = exp2_fast(st[u].x - zero);
       sum += st[u].y * f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) z[e] += x[u][e >> 2][e & 3] * f;
+      for (int e = 0; e < E; ++e) z[e] += x[u][e] * f;
     }
+  };
+  auto store = [&](int at, int e0, float top, float sum, const auto &z) {
+    const int group = at / kBlocks, b = at % kBlocks, at_row = group * kCols + c;
+    if (at_row >= in.count) return;
+    const int m = in.m0 + at_row, i = m / g.per;
+    const int64_t row = (int64_t)(in.from + i) * a.q_heads + in.kvh * g.per + (m - i * g.per);
+    const float over = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int e = 0; e < (int)(sizeof(z) / sizeof(z[0])); ++e)
+      st_global<f32x4>(a.out + row * D + 32 * b + 8 * (e0 + e) + 4 * h, z[e] * over);
+    if (a.lse && b == 0 && e0 == 0 && h == 0) a.lse[row] = row_lse(top, sum);
+  };
+  constexpr f32x4 kZero = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (in.parts < kMany) {
+    for (int at = 4 * helper + wave; at < blocks; at += 4 * helpers) {
+      float top = -INFINITY, sum = 0.0f;
+      f32x4 z[4] = {kZero, kZero, kZero, kZero};
+      for (int p = 0; p < in.parts; p += 8)
+        add(std::integral_constant<int, 8>{}, at, 0, p, 1, top, sum, z);
+      store(at, 0, top, sum, z);
+    }
+    return;
   }
-  if (at_row >= in.count) return;
-  const int m = in.m0 + at_row, i = m / g.per;
-  const int64_t row = (int64_t)(in.from + i) * a.q_heads + in.kvh * g.per + (m - i * g.per);
-  store_block(a.out + row * D + 32 * b + 4 * h, z, sum > 0.0f ? 1.0f / sum : 0.0f);
-  if (a.lse && b == 0 && h == 0) a.lse[row] = row_lse(top, sum);
+  for (int unit = helper; unit < 4 * blocks; unit += helpers) {
+    const int at = unit >> 2, e = unit & 3;
+    float top = -INFINITY, sum = 0.0f;
+    f32x4 z[1] = {kZero};
+    for (int p = wave; p < in.parts; p += 4 * 16)
+      add(std::integral_constant<int, 16>{}, at, e, p, 4, top, sum, z);
+    sh_z[wave][lane] = z[0];
+    sh_st[wave][lane] = f32x2{top, sum};
+    __syncthreads();
+    if (wave == 0) {
+      float all = -INFINITY;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) all = fmaxf(all, sh_st[s][lane].x);
+      const float zero = all == -INFINITY ? 0.0f : all;
+      sum = 0.0f;
+      z[0] = kZero;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const float f = exp2_fast(sh_st[s][lane].x - zero);
+        sum += sh_st[s][lane].y * f;
+        z[0] += sh_z[s][lane] * f;
+      }
+      store(at, e, all, sum, z);
+    }
+    __syncthreads();
+  }
 }
 
 template <int DT, int D>
@@ -985,7 +1039,7 @@ void chunk_requests(const ChunkArgs &a, const ChunkGrid &g, hipStream_t stream) 
   else
     chunk_kernel<DT, D, false, false><<<g.groups, threads_of(D), 0, stream>>>(a, g);
   if (g.groups > 1)   // (else nothing is cut)
-    join_kernel<D><<<dim3(g.groups, kRows / kCols), 2 * D, 0, stream>>>(a, g);
+    join_kernel<D><<<dim3(2 * g.groups, kHelpers), 256, 0, stream>>>(a, g);
 }
 
 template <int DT>
