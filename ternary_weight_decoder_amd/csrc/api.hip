@@ -1278,8 +1278,8 @@ bitnet_status bitnet_add_rms_norm(int64_t M, int64_t K, const float *x, int64_t 
       !aligned(y, 16) || !aligned(xq, 16) || !aligned(x_scale, 4))
     return BITNET_ERR_ALIGN;
   // The sum may take the place of one of its terms.
-  const bool on_x = sum_out == x && x_stride == K;
-  const bool on_r = sum_out == residual && residual_stride == K;
+  const bool on_x = sum_out == x && (x_stride == K || M == 1);
+  const bool on_r = sum_out == residual && (residual_stride == K || M == 1);
   const Range r[] = {{sum_out, M * K * 4},
                      {y, M * K * 4},
                      {xq, M * K},
@@ -1318,7 +1318,8 @@ bitnet_status bitnet_silu_mul(int64_t M, int64_t K, const float *gate, int64_t g
       !aligned(y, 16) || !aligned(xq, 16) || !aligned(x_scale, 4))
     return BITNET_ERR_ALIGN;
   // y may take the place of one of its factors.
-  const bool on_g = y == gate && gate_stride == K, on_u = y == up && up_stride == K;
+  const bool on_g = y == gate && (gate_stride == K || M == 1);
+  const bool on_u = y == up && (up_stride == K || M == 1);
   const Range r[] = {{y, M * K * 4},
                      {xq, M * K},
                      {x_scale, M * 4},

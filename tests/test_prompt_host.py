@@ -111,6 +111,14 @@ def test_norm_passes(L):
     assert norm(L, M=0) == 0
 
 
+def test_one_row_in_place_whatever_its_stride(L):
+    """A single row is contiguous."""
+    for kw in (dict(s=A, xs=68), dict(s=A + GB, rs=128)):
+        assert norm(L, M=1, **kw) in PASSED and norm(L, M=2, **kw) == ALIAS
+    for kw in (dict(y=A, gs=68), dict(y=A + GB, us=128)):
+        assert gate(L, M=1, **kw) in PASSED and gate(L, M=2, **kw) == ALIAS
+
+
 def gate(L, M=4, K=64, g=A, gs=64, u=A + GB, us=64, y=A + 2 * GB, xq=A + 3 * GB, sc=A + 4 * GB):
     return L.bitnet_silu_mul(M, K, g, gs, u, us, y, xq, sc, None)
 
