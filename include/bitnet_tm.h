@@ -676,8 +676,8 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
  *   heads, lse and what has to be finite as for bitnet_paged_attention (which it
  *   equals within both calls' errors), and the precision too, except that with
  *   fp16 and int8 caches what lies below 2^-33 of the largest probability (times
- *   the largest value scale) may count as zero, and that an 8-bit row whose value
- *   scale is not finite does.  A token has no influence on rows that come before
+ *   the largest value scale, or 2^-100) may count as zero, and that an 8-bit row
+ *   whose value scale is not finite does; 8-bit values stay below 2^100.  A token has no influence on rows that come before
  *   it, whatever it holds.
  *   starts int32 [R+1] (bitnet_kv_map's) and lens int32 [R] (its state's first
  *   entries) are device data.  Starts are taken in ascending order (each as

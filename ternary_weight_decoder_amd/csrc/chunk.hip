@@ -306,8 +306,8 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
   constexpr int kTile = S::kTile, kWaves = S::kWaves, kThreads = S::kThreads, kSplit = S::kSplit;
   // Probabilities are relative to 2^-kUp of a base that the running maximum
   // exceeds by up to 2^kSlack, so that it need not follow every new maximum.  With
-  // 8-bit values the maximum is that of probability times scale, and the values
-  // that the products take are bare codes.
+  // 8-bit values the products take bare codes, and probabilities times scales, relative
+  // to 2^v_base above the largest scale so far.
   constexpr float kSlack = 6.0f, kUp = F::kHalf ? 15.0f - kSlack : 0.0f;
   typedef ChunkShared<DT, D, FEW> Sh;
   __shared__ Sh sh;
@@ -653,6 +653,7 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
     }
 
     float base = -INFINITY, l = 0.0f;   // of the exponents, without kUp
+    float v_base = -126.0f;             // 8-bit caches: exponent of the outputs' unit
     f32x16 o[kBlocks];
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
@@ -731,7 +732,7 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
         }
       };
       // Exponent above the largest of the values' scales that the row sees.
-      float v_exp = 0.0f;
+      float v_exp = -126.0f;
       if constexpr (kI8) {
         v_exp = v_exp0;
         if (!all) {
@@ -758,12 +759,17 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
       float top = x[0];
 #pragma unroll
       for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
-      top = max2(top) * unscale + v_exp;
-      if (__any(top > base + kSlack)) {
+      top = max2(top) * unscale;
+      if (__any(top > base + kSlack || (kI8 && v_exp > v_base))) {
         const float b_new = fmaxf(base, top);
-        const float keep = base == -INFINITY ? 0.0f : exp2_fast(base - b_new);
+        float keep = base == -INFINITY ? 0.0f : exp2_fast(base - b_new);
         base = b_new;
         l *= keep;
+        if constexpr (kI8) {
+          const float v_new = fmaxf(v_base, v_exp);
+          keep *= exp2_fast(v_base - v_new);
+          v_base = v_new;
+        }
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) o[b] *= keep;
       }
@@ -780,9 +786,11 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
         float vs[16];
         __builtin_amdgcn_sched_barrier(0);   // (asked for earlier they take registers too many)
         scales(1, vs);
-        // (A scale above that of all that the row sees goes with a probability of zero.)
+        // (A scale above that of all that the row sees goes with a probability of zero,
+        // which comes first, so that the product is zero.)
+        const float over = exp2_fast(-v_base);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] *= vs[e];
+        for (int e = 0; e < 16; ++e) x[e] = x[e] * over * vs[e];
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -846,6 +854,11 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
       if (kSplit == 2 && part == 0) __syncthreads();
     }
     l = sum2(l);
+    if constexpr (kI8) {
+      const float unit = exp2_fast(v_base);
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) o[b] *= unit;
+    }
     // The groups of waves join: of a pair each wave keeps half of the channels.
     constexpr int kMine = S::kMine;   // channel blocks, from b0 on
     const int b0 = part * kMine;

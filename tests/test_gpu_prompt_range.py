@@ -268,3 +268,71 @@ def test_logprobs_largest_vocabulary(tb, gen, top):  # noqa: F811
         assert host(got["top_tokens"])[0].tolist() == best[:top]
         w = np.arange(60, 60 - top, -1) / 4 - lse
         assert (np.abs(host(got["top_logprobs"])[0] - w) <= e + U * np.abs(w)).all()
+
+
+# ---- chunk attention: scales and magnitudes -----------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "int8"])
+@pytest.mark.parametrize("scale", [0.0, -0.0, -0.25, 1e-30, -3.0])
+def test_chunk_of_any_scale(tb, dtype, scale):  # noqa: F811
+    chunk_case(tb, 31, dtype, [70, 1, 33], [300, 64, 0], 2, 3, 128, 16, scale=scale)
+
+
+@pytest.mark.parametrize("q2,k2,v2", [(-100, 100, 0), (118, -118, 0), (100, -100, -110), (0, 0, 120),
+                                      (58, 58, 0), (50, 50, 100)])
+@pytest.mark.parametrize("D", [64, 256])
+def test_chunk_of_any_magnitude(tb, D, q2, k2, v2):  # noqa: F811
+    """bf16 caches near the ends of fp32: queries 2^-100 to 2^118, scores up to 2^122."""
+    import torch
+    from tests.test_gpu_prompt import run_chunk
+    say(f"[prompt range] chunk of q 2^{q2}, k 2^{k2}, v 2^{v2}")
+    rng = np.random.default_rng(6)
+    new, old = np.array([70, 1, 40]), np.array([0, 32, 560])
+    pg = Paged(tb, rng, "bf16", new + old, 2, D, 16)
+    for t, f in ((pg.kd, k2), (pg.vd, v2)):
+        t.copy_(torch.ldexp(t.float(), torch.tensor(f, device="cuda:0")).bfloat16())
+    pg.make(tb)
+    q = rng.normal(0, 1, (111, 6, D)).astype(np.float32) * np.float32(2.0 ** q2)
+    run_chunk(tb, pg, q, np.r_[0, np.cumsum(new)], new + old, 6, scale=0.125)
+
+
+@pytest.mark.parametrize("k2,v2,uneven", [(0, 0, 20), (-90, 0, 0), (60, 0, 0), (0, -90, 0), (0, 90, 0),
+                                          (0, -60, 30), (0, 0, 0)])
+def test_chunk_of_any_scales_of_rows(tb, k2, v2, uneven):  # noqa: F811
+    """8-bit caches: scales far from one, value scales up to 2^`uneven` apart, zeros."""
+    from tests.test_gpu_prompt import run_chunk
+    say(f"[prompt range] chunk of row scales 2^{k2}, 2^{v2}, {uneven} apart")
+    rng = np.random.default_rng(8)
+    new, old = np.array([70, 1, 40]), np.array([0, 90, 300])
+    pg = Paged(tb, rng, "int8", new + old, 2, 128, 16)
+    pg.ksd *= 2.0 ** k2
+    pg.vsd *= dev((2.0 ** v2 * 2.0 ** -rng.integers(0, uneven + 1, pg.vsd.shape)).astype(np.float32))
+    pg.vsd[0, ::3] = 0
+    pg.ks, pg.vs = host(pg.ksd), host(pg.vsd)
+    pg.make(tb)
+    q = (rng.normal(0, 1, (111, 12, 128)) * 2.0 ** -k2).astype(np.float32)
+    run_chunk(tb, pg, q, np.r_[0, np.cumsum(new)], new + old, 12)
+
+
+def test_chunk_scores_of_thousands(tb):  # noqa: F811
+    """Scores of thousands, rising and falling along the length: the base moves often."""
+    import torch
+    from tests.test_gpu_prompt import run_chunk
+    rng = np.random.default_rng(9)
+    for dtype in ("bf16", "fp16", "int8"):
+        for order in (1, -1):
+            say(f"[prompt range] rising scores {dtype} {order}")
+            pg = Paged(tb, rng, dtype, [700], 1, 128, 32)
+            ramp = torch.linspace(*((0.2, 4) if order > 0 else (4, 0.2)), 736, device="cuda:0")
+            for j in range(-(-700 // 32)):
+                page = int(pg.tables[0, j])
+                row = ramp[32 * j:32 * j + 32]
+                if dtype == "int8":
+                    pg.ksd[0, page, 0] = row * 0.03
+                else:
+                    pg.kd[0, page, 0] *= row[:, None].to(pg.kd.dtype)
+            if dtype == "int8":
+                pg.ks = host(pg.ksd)
+            pg.make(tb)
+            q = (40 * rng.normal(0, 1, (90, 6, 128))).astype(np.float32)
+            run_chunk(tb, pg, q, [0, 90], [700], 6, scale=0.5)
