@@ -677,8 +677,8 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
  *   equals within both calls' errors), and the precision too, except that with
  *   fp16 and int8 caches what lies below 2^-33 of the largest probability (times
  *   the largest value scale, or 2^-100) may count as zero, and that an 8-bit row
- *   whose value scale is not finite does; 8-bit values stay below 2^100.  A token has no influence on rows that come before
- *   it, whatever it holds.
+ *   whose value scale is not finite does; 8-bit values stay below 2^100.  A token
+ *   has no influence on rows that come before it, whatever it holds.
  *   starts int32 [R+1] (bitnet_kv_map's) and lens int32 [R] (its state's first
  *   entries) are device data.  Starts are taken in ascending order (each as
  *   the largest up to it) and clamped to [0, T], lengths to [0, max_len].  A
@@ -774,8 +774,9 @@ bitnet_status bitnet_beam_reorder(const bitnet_kv_cache *cache, int64_t B, int64
  * before the feed-forward part, gate * sigmoid(gate) * up inside it).
  * Outputs are fp32 rows y, 8-bit rows xq with a scale each, or both (at least one;
  * NULL for the other; xq and x_scale go together): xq, x_scale are exactly
- * bitnet_quant_act of y, the form bitnet_ternary_matmul_q8 takes (M > 16);
- * the decode projections (M <= 16) take y.
+ * bitnet_quant_act of y, the form bitnet_ternary_matmul_q8 takes; the decode
+ * projections (M <= 16) of bitnet_ternary_matmul and its grouped forms quantize y
+ * themselves, in the same launch.
  *
  * bitnet_add_rms_norm: h = fl32(x + residual) (residual NULL: h = x),
  *     y = fl32(h * weight / sqrt(mean_k h^2 + eps)),
