@@ -38,7 +38,7 @@
 // rows: a linear function of the tile's number, so every place on the line has
 // a closed form and no list of items is made.  What an item's beginning and end
 // cost (queries as terms, the first tiles' way from memory, the joining) counts as
-// kFixed tokens.  A stretch may hold the end of an item, whole ones and the
+// some 200 tokens.  A stretch may hold the end of an item, whole ones and the
 // beginning of another; the parts of items that are cut go to the workspace, and a
 // second launch joins them.  (Its launch takes 2 us and what it reads and writes 2
 // of a tail of 4 tokens, 6 of a prompt of 1800, near HBM's rate.)
@@ -75,9 +75,12 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 // Workgroups, one a compute unit (512: the prompt of 1800 tokens 58 us, 48 with 256).
 constexpr int kGrid = 256;
-// Tokens that an item's beginning and end cost as much as (96, 192, 256, 384: that
-// prompt 58, 49.6, 46.4, 45.1 us, 16 ragged requests 75, 63.4, 63.7, 65.3).
-constexpr int kFixed = 256;
+// Tokens that an item's beginning and end cost as much as (128 channels: 96, 192, 256,
+// 384: that prompt 58, 49.6, 46.4, 45.1 us, 16 ragged requests 75, 63.4, 63.7, 65.3; 64
+// channels: 256, 320, 384, 512: 36, 37, 38, 37 and 54, 52.5, 53, 58; 256 channels, whose
+// tokens take longer: 64, 128, 160, 256: 113, 94, 94.6, 101, and 22 requests of some 220
+// fp16 tokens 58, 56, 53.7, 51).
+constexpr int fixed_of(int D) { return D == 256 ? 160 : 256; }
 // Tiles of a stretch, at least (1, 2, 4: a tail of 4 tokens 15.1, 14.6, 17.0 us).
 constexpr int kLeast = 2;
 
@@ -97,7 +100,7 @@ ChunkPlan chunk_plan(int64_t T, int64_t R, int64_t q_heads, int64_t kv_heads, in
   const int64_t items = kv_heads * (T * (q_heads / kv_heads) / kRows + R);
   const int64_t tile = kBlock * split_of((int)D), tiles = (max_len + tile - 1) / tile;
   ChunkPlan p;
-  p.groups = (int)std::min<int64_t>(kGrid, items * (tiles + kFixed / tile));
+  p.groups = (int)std::min<int64_t>(kGrid, items * (tiles + fixed_of((int)D) / tile));
   // Two places a workgroup: for the item at its beginning and the one at its end.
   const size_t rows = 2 * (size_t)p.groups * kRows;
   p.outs = 2 * kGrid * sizeof(Record);
@@ -260,6 +263,7 @@ struct ChunkGrid {
 };
 
 // From the largest start up to this request's, which is the next one's at least.
+template <int D>
 __device__ __forceinline__ Request request_of(const ChunkArgs &a, int per, int start, int next,
                                               int len) {
   Request q;
@@ -268,7 +272,7 @@ __device__ __forceinline__ Request request_of(const ChunkArgs &a, int per, int s
   q.old = min(max(len, 0), a.max_len) - q.n;
   const int rows = q.n * per;
   q.tiles = (rows + kRows - 1) / kRows;
-  q.lead = (double)(max(q.old, 0) + kFixed) * per;
+  q.lead = (double)(max(q.old, 0) + fixed_of(D)) * per;
   q.line = q.tiles == 0 ? 0.0
                         : q.tiles * q.lead + (double)(kRows / 2) * q.tiles * (q.tiles - 1) + rows;
   return q;
@@ -324,7 +328,7 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
     const int r = min(lane, a.R - 1);
     const int start = ld_global<int>(a.starts + r), next = ld_global<int>(a.starts + r + 1);
     const int len = ld_global<int>(a.lens + r);
-    Request mine = request_of(a, per, scan_max(max(start, 0)), next, len);
+    Request mine = request_of<D>(a, per, scan_max(max(start, 0)), next, len);
     if (lane >= a.R) mine.line = 0.0;
     const double upto = scan_sum(mine.line * kv_heads);
     total = read_lane(upto, 63);
@@ -347,7 +351,7 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
     double sum = 0.0;
     for (int r = r0; r < r1; ++r) {
       top = max(top, ld_global<int>(a.starts + r));
-      sum += request_of(a, per, top, ld_global<int>(a.starts + r + 1), ld_global<int>(a.lens + r)).line *
+      sum += request_of<D>(a, per, top, ld_global<int>(a.starts + r + 1), ld_global<int>(a.lens + r)).line *
              kv_heads;
     }
     const double all = scan_sum(sum);
@@ -396,7 +400,7 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
       r = at * each;
       for (;;) {
         top = max(top, ld_global<int>(a.starts + r));
-        q = request_of(a, per, top, ld_global<int>(a.starts + r + 1), ld_global<int>(a.lens + r));
+        q = request_of<D>(a, per, top, ld_global<int>(a.starts + r + 1), ld_global<int>(a.lens + r));
         const double next = from + q.line * kv_heads;
         if (pos < next || r + 1 >= min(at * each + each, a.R)) break;
         from = next;
@@ -429,7 +433,7 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
     const int len = min(max(old + (m0 + count - 1) / per + 1, 0), a.max_len);   // that the last row sees
     const int tiles = (len + kTile - 1) / kTile;
     // Tiles [first, end) of the item are this stretch's.
-    const double tile_at = item0 + (double)kFixed * per;   // the place of the first
+    const double tile_at = item0 + (double)fixed_of(D) * per;   // the place of the first
     auto cut = [&](double at) {
       return at <= tile_at ? 0 : (int)fmin(quotient(at - tile_at, unit, g.over_unit), (double)tiles);
     };
