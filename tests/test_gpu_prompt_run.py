@@ -305,3 +305,49 @@ def test_two_graphs_with_a_workspace_each(tb):  # noqa: F811
                 graphs[n].replay()
         torch.cuda.synchronize()
         assert [[host(t).tobytes() for t in o] for o in outs] == wants, turn
+
+
+def test_layer_of_the_readme(tb):  # noqa: F811
+    """The README's layer around the projections, as it stands there, behind its page map."""
+    import os
+    import re
+    import torch
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md")) as f:
+        found = [b for b in re.findall(r"```python\n(.*?)```", f.read(), re.S)
+                 if "bitnet_chunk_attention" in b]
+    assert len(found) == 1
+    say("[prompt run] the README's layer")
+    rng = np.random.default_rng(4)
+    f = lambda *s: dev(rng.normal(0, 1, s).astype(np.float32))
+    w = lambda n, k: (*tb.bitnet_ternarize_pack(f(n, k)), n)
+    rows, new = 16, rng.integers(0, 40, 16).astype(np.int32)
+    T = int(new.sum())
+    cache = tb.KvCache.empty(2, 128, KV, PS, D)
+    pool, state = tb.KvPool.empty(rows, 8, 128, PS)
+    step = tb.bitnet_kv_map(pool, T, dev(new), state)
+    cos, sin = (dev(a) for a in rope_tables(64, D))
+    ns = {"tb": tb, "cache": cache, "layer": 1, "pool": pool, "state": state, "step": step,
+          "cos": cos, "sin": sin, "x": f(T, HID), "delta": f(T, HID), "norm1": f(HID),
+          "norm2": f(HID), "wq": w(H * D, HID), "wk": w(KV * D, HID), "wv": w(KV * D, HID),
+          "wo": w(HID, H * D), "wg": w(FF, HID), "wu": w(FF, HID), "wd": w(HID, FF),
+          "logits": f(T, V), "following": dev(rng.integers(0, V, T).astype(np.int32))}
+    x, delta = host(ns["x"]), host(ns["delta"])
+    exec(found[0], ns)
+    d = Decoder(tb, "bf16")
+    d.cache, d.pool, d.state = cache, pool, state
+    lens = host(state)[:rows]
+    assert (lens == new).all()
+    held = [[d.held(s, 1, r, n) for r, n in enumerate(lens)] for s in (0, 1)]
+    got = ref.chunk_attention(host(ns["q"]).reshape(-1, H, D), host(step["starts"]), lens, 64,
+                              lambda r, n: held[0][r][:, :n], lambda r, n: held[1][r][:, :n], D ** -0.5)
+    a = host(ns["a"]).reshape(-1, H, D)
+    for t, (want, _, smax, mag, n) in got.items():
+        lost = n * LOST["bf16"] * max(np.abs(v).max(initial=0) for v in held[1])
+        tol = U * (2 * (D + 16) * smax + 2 * n + 64)[:, None] * mag + lost
+        assert (np.abs(a[t] - want) <= tol).all(), t
+    back = host(ns["x"]) - host(tb.bitnet_ternary_matmul(ns["a"], *ns["wo"]))
+    assert np.allclose(back, x + delta, atol=1e-3)
+    Check(d).codes(ns["h"], ref.silu_mul(host(ns["gate"]), host(ns["up"])))
+    Check(d).score(ns["logits"], ns["following"], ns["scores"])
+    assert torch.isfinite(ns["delta"]).all()
