@@ -612,9 +612,9 @@ bitnet_status bitnet_kv_map(const bitnet_kv_pool *pool, int64_t T, const int32_t
  *   A token whose slot is outside [0, pages*page_size), or whose position is
  *   outside [0, max_pos) where it is used, is skipped: nothing of it is
  *   written, q_out included.  Slots of one call must differ from each other.
- *   T == 0 launches nothing.  q_out == q is allowed for contiguous rows; other
- *   overlaps of q_out, and inputs inside the layer's elements or scales, are
- *   BITNET_ERR_ALIAS.  q, k, v, q_out, cos and sin 16-byte
+ *   T == 0 launches nothing.  q_out == q is allowed for contiguous rows (a single
+ *   row is contiguous whatever q_stride says); other overlaps of q_out, and
+ *   inputs inside the layer's elements or scales, are BITNET_ERR_ALIAS.  q, k, v, q_out, cos and sin 16-byte
  *   aligned, row strides multiples of 4 and below 2^31 elements; T,
  *   q_heads*head_dim and max_pos below 2^23.  One launch.
  */

@@ -1003,7 +1003,7 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, int32_t layer, int6
       (rotate && (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(positions, 4))) ||
       (q && (!aligned(q, 16) || !aligned(q_out, 16))))
     return BITNET_ERR_ALIGN;
-  const bool in_place = q_out == q && q_stride == qd;
+  const bool in_place = q_out == q && (q_stride == qd || T == 1);
   const Range r[] = {{q_out, T * qd * 4},
                      {in_place ? nullptr : q, q ? ((T - 1) * q_stride + qd) * 4 : 0},
                      {k, ((T - 1) * k_stride + kd) * 4},
