@@ -48,10 +48,15 @@ __device__ __forceinline__ bool huge(float m) { return fabsf(m) > 0x1p20f; }
 __device__ __forceinline__ double exponent(float m) {
   return huge(m) ? (double)m * (double)kLog2e : (double)(m * kLog2e);
 }
-// The difference of two maxima's exponents, m <= n, n > -inf, and its exp2.
+// The difference of two maxima's exponents, m <= n, n > -inf, and its exp2.  An fma
+// gives a rounded product's difference to an exact one; of two large maxima the
+// difference itself is exact where its exp2 is not zero.  (Selects: with a branch to
+// fp64 16 groups of 4 beams of 32,000 logits take 11.4 us, 11.2 so.)
 __device__ __forceinline__ float rise(float m, float n) {
-  if (huge(n) || (huge(m) && m > -INFINITY)) return (float)(exponent(m) - exponent(n));
-  return m * kLog2e - n * kLog2e;
+  const float mc = m * kLog2e, nc = n * kLog2e;
+  const float to_near = huge(m) ? __builtin_fmaf(m, kLog2e, -nc) : mc - nc;
+  const float to_far = huge(m) ? (m - n) * kLog2e : -__builtin_fmaf(n, kLog2e, -mc);
+  return huge(n) ? to_far : to_near;
 }
 __device__ __forceinline__ float shift(float m, float n) {
   return __builtin_amdgcn_exp2f(rise(m, n));
