@@ -638,7 +638,17 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
           for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[f][e >> 2][e & 3]));
         const float p2 = pow2_above(max2(big) * fabsf(up));
         unscale = p2 * 0x1p-14f;
-        up *= pow2_inverse(p2) * 0x1p14f;   // (exact)
+        const float to_half = pow2_inverse(p2) * 0x1p14f;
+        // Both in one factor, which is exact, unless tiny queries meet so large a scale
+        // that it is infinite: those are below 2^-113 and raised first.
+        const bool tiny = fabsf(up * to_half) == INFINITY;
+        if (__any(tiny)) {
+#pragma unroll
+          for (int f = 0; f < kSteps; ++f)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[f][e >> 2][e & 3] *= tiny ? 0x1p120f : 1.0f;
+        }
+        up = (tiny ? up * 0x1p-120f : up) * to_half;
       }
 #pragma unroll
       for (int f = 0; f < kSteps; ++f) {
