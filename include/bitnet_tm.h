@@ -647,7 +647,8 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, int32_t layer, int6
  *   below 2^23, T * kv_heads (times 2, 3, 4 for more than 16, 32, 48 query
  *   heads per kv head) and max_pages below 2^31, max_len below 2^30; q and out
  *   16-byte aligned, q_stride a multiple of 4 and below 2^31.
- *   q and the tokens in use are finite, scale is finite (else BITNET_ERR_SHAPE),
+ *   q and the tokens in use are finite, scale * log2(e) is finite in fp32 (else
+ *   BITNET_ERR_SHAPE; of a scale below 2^-126 the bits that fp32 has there count),
  *   and scale * q and scale * sum_i |q_i k_ji| stay below 2^125; rows that
  *   break this give unspecified outputs of their own and leave the others alone.
  *   T == 0 launches nothing.  out, lse and workspace must overlap neither each

@@ -1044,6 +1044,9 @@ static bool attend_shape_ok(int64_t T, int64_t q_heads, int64_t kv_heads, int64_
   return (D == 64 || D == 128 || D == 256) && max_len >= 1 && max_len < kLimit / 2;
 }
 
+// The kernels take scores in units of log 2.
+static bool scale_ok(float scale) { return std::isfinite(scale * 1.44269504088896340736f); }
+
 size_t bitnet_paged_attention_workspace_bytes(int64_t T, int64_t q_heads, int64_t kv_heads,
                                               int64_t head_dim, int64_t max_len) {
   if (!attend_shape_ok(T, q_heads, kv_heads, head_dim, max_len)) return 0;
@@ -1064,7 +1067,7 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
   if (!attend_shape_ok(T, q_heads, cache->kv_heads, D, max_len) || q_stride < qd ||
       q_stride >= kLimit || table_rows < 1 || table_rows >= kMaxTokens || max_pages < 1 ||
       max_pages >= kLimit || max_len > max_pages * cache->page_size ||
-      (!rows && T > table_rows) || !std::isfinite(scale))
+      (!rows && T > table_rows) || !scale_ok(scale))
     return BITNET_ERR_SHAPE;
   if (q_stride % 4 || !aligned(q, 16) || !aligned(out, 16) || !aligned(tables, 4) ||
       !aligned(lens, 4) || (rows && !aligned(rows, 4)) || (lse && !aligned(lse, 4)))
@@ -1130,7 +1133,7 @@ bitnet_status bitnet_chunk_attention(const bitnet_kv_cache *cache, int32_t layer
   const int64_t D = cache->head_dim, qd = q_heads * D;
   if (!chunk_shape_ok(T, R, q_heads, cache->kv_heads, D, max_len) || q_stride < qd ||
       q_stride >= kLimit || max_pages < 1 || max_pages >= kLimit ||
-      max_len > max_pages * cache->page_size || !std::isfinite(scale))
+      max_len > max_pages * cache->page_size || !scale_ok(scale))
     return BITNET_ERR_SHAPE;
   if (q_stride % 4 || !aligned(q, 16) || !aligned(out, 16) || !aligned(starts, 4) ||
       !aligned(lens, 4) || !aligned(tables, 4) || (lse && !aligned(lse, 4)))
