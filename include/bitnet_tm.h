@@ -651,6 +651,8 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, int32_t layer, int6
  *   BITNET_ERR_SHAPE; of a scale below 2^-126 the bits that fp32 has there count),
  *   and scale * q and scale * sum_i |q_i k_ji| stay below 2^125; rows that
  *   break this give unspecified outputs of their own and leave the others alone.
+ *   So do rows that attend to 8-bit keys of 2^100 and more, or to values of a
+ *   channel whose magnitudes sum up to 2^127 (bf16) or 2^113 (int8).
  *   T == 0 launches nothing.  out, lse and workspace must overlap neither each
  *   other, nor the inputs, nor the layer.
  *   workspace: bitnet_paged_attention_workspace_bytes(...) bytes, 256-byte
@@ -678,8 +680,10 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
  *   equals within both calls' errors), and the precision too, except that with
  *   fp16 and int8 caches what lies below 2^-33 of the largest probability (times
  *   the largest value scale, or 2^-100) may count as zero, and that an 8-bit row
- *   whose value scale is not finite does; 8-bit values stay below 2^100.  A token
- *   has no influence on rows that come before it, whatever it holds.
+ *   whose value scale is not finite does.  8-bit keys and values stay below 2^100
+ *   (at any length), and the magnitudes of a channel's bf16 values that a row
+ *   attends to sum up to less than 2^121.  A token has no influence on rows that
+ *   come before it, whatever it holds.
  *   starts int32 [R+1] (bitnet_kv_map's) and lens int32 [R] (its state's first
  *   entries) are device data.  Starts are taken in ascending order (each as
  *   the largest up to it) and clamped to [0, T], lengths to [0, max_len].  A

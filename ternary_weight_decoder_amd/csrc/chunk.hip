@@ -81,12 +81,14 @@ constexpr int kGrid = 256;
 // tokens take longer: 64, 128, 160, 256: 113, 94, 94.6, 101, and 22 requests of some 220
 // fp16 tokens 58, 56, 53.7, 51).
 constexpr int fixed_of(int D) { return D == 256 ? 160 : 256; }
+// 8-bit caches: exponent of the outputs' unit before there is a value.
+constexpr float kNoUnit = -126.0f;
 // Tiles of a stretch, at least (1, 2, 4: a tail of 4 tokens 15.1, 14.6, 17.0 us).
 constexpr int kLeast = 2;
 
 struct ChunkPlan {
   int groups;
-  size_t outs, stats, total;   // workspace offsets; records first
+  size_t outs, stats, units, total;   // workspace offsets; records first
 };
 // Of a place in the workspace, of which a workgroup has two: the item of which it holds
 // a part (parts: 0 for none).  The parts' places are `place`, then every second one from
@@ -105,7 +107,8 @@ ChunkPlan chunk_plan(int64_t T, int64_t R, int64_t q_heads, int64_t kv_heads, in
   const size_t rows = 2 * (size_t)p.groups * kRows;
   p.outs = 2 * kGrid * sizeof(Record);
   p.stats = p.outs + rows * D * 4;
-  p.total = p.stats + rows * 8;
+  p.units = p.stats + rows * 8;
+  p.total = p.units + rows * 4;
   return p;
 }
 
@@ -246,7 +249,7 @@ struct ChunkShared {
                                          (S::kSplit - 1) * S::kWaves * S::kMine * 4096);
   __attribute__((aligned(16))) uint8_t kv[kBytes];
   __attribute__((aligned(16))) uint8_t q[S::kKept < S::kTerms ? S::kWaves * 64 * D : 16];
-  float stats[S::kWaves][2][kCols];        // and their bases and sums
+  float stats[S::kWaves][DT == BITNET_KV_INT8 ? 3 : 2][kCols];   // and their bases, sums, units
   int pages[S::kWaves][64];
   float scales[S::kWaves][2][2][kBlock];   // 8-bit caches: two blocks' key and value scales
   double first[FEW ? 64 : S::kThreads];    // places before each request, or each thread's
@@ -257,7 +260,7 @@ struct ChunkShared {
 };
 
 struct ChunkGrid {
-  int64_t outs_off, stats_off;     // in the workspace
+  int64_t outs_off, stats_off, units_off;   // in the workspace
   double over_groups, over_unit;   // 1 / workgroups, 1 / (a tile of tokens' places)
   int32_t groups, per;   // workgroups; query heads per key/value head
 };
@@ -278,12 +281,14 @@ __device__ __forceinline__ Request request_of(const ChunkArgs &a, int per, int s
   return q;
 }
 
-// 16 of a row's 32 channels of a block, times `over`.
-__device__ __forceinline__ void store_block(float *out, const f32x16 &y, float over) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    st_global<f32x4>(out + 8 * e, f32x4{y[4 * e] * over, y[4 * e + 1] * over, y[4 * e + 2] * over,
-                                        y[4 * e + 3] * over});
+// What a row has summed up, times the reciprocal of its probabilities' sum, and of 8-bit
+// caches times its unit, 2^unit.  (Not the sums times the unit: those pass the largest
+// value by up to 2^15 a token.)
+template <bool I8>
+__device__ __forceinline__ f32x4 mean_of(f32x4 y, float over, float unit) {
+  y *= over;
+  if constexpr (I8) y *= exp2_fast(unit);
+  return y;
 }
 // Exponent of the power of two above x >= 0, at least -100.
 __device__ __forceinline__ float exponent_above(float x) {
@@ -667,7 +672,7 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
     }
 
     float base = -INFINITY, l = 0.0f;   // of the exponents, without kUp
-    float v_base = -126.0f;             // 8-bit caches: exponent of the outputs' unit
+    float v_base = kNoUnit;             // 8-bit caches: exponent of the outputs' unit
     f32x16 o[kBlocks];
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
@@ -746,7 +751,7 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
         }
       };
       // Exponent above the largest of the values' scales that the row sees.
-      float v_exp = -126.0f;
+      float v_exp = kNoUnit;
       if constexpr (kI8) {
         v_exp = v_exp0;
         if (!all) {
@@ -868,11 +873,6 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
       if (kSplit == 2 && part == 0) __syncthreads();
     }
     l = sum2(l);
-    if constexpr (kI8) {
-      const float unit = exp2_fast(v_base);
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) o[b] *= unit;
-    }
     // The groups of waves join: of a pair each wave keeps half of the channels.
     constexpr int kMine = S::kMine;   // channel blocks, from b0 on
     const int b0 = part * kMine;
@@ -892,13 +892,20 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
       if (h == 0) {
         sh.stats[wave][0][c] = base;
         sh.stats[wave][1][c] = l;
+        if constexpr (kI8) sh.stats[wave][2][c] = v_base;
       }
       __syncthreads();
       const float base2 = sh.stats[wave ^ kRowWaves][0][c], l2 = sh.stats[wave ^ kRowWaves][1][c];
       const float top = fmaxf(base, base2), zero = top == -INFINITY ? 0.0f : top;
-      const float f1 = exp2_fast(base - zero), f2 = exp2_fast(base2 - zero);
+      float f1 = exp2_fast(base - zero), f2 = exp2_fast(base2 - zero);
       base = top;
       l = l * f1 + l2 * f2;
+      if constexpr (kI8) {
+        const float v2 = sh.stats[wave ^ kRowWaves][2][c], v_top = fmaxf(v_base, v2);
+        f1 *= exp2_fast(v_base - v_top);
+        f2 *= exp2_fast(v2 - v_top);
+        v_base = v_top;
+      }
 #pragma unroll
       for (int b = 0; b < kMine; ++b)
 #pragma unroll
@@ -922,7 +929,11 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
         const float over = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
         for (int b = 0; b < kMine; ++b)
-          store_block(a.out + row * D + 32 * (b0 + b) + 4 * h, y[b], over);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)   // 16 of a row's 32 channels of a block
+            st_global<f32x4>(a.out + row * D + 32 * (b0 + b) + 4 * h + 8 * e,
+                             mean_of<kI8>(f32x4{y[b][4 * e], y[b][4 * e + 1], y[b][4 * e + 2], y[b][4 * e + 3]},
+                                          over, v_base));
         if (a.lse && h == 0 && part == 0) a.lse[row] = row_lse(base - kUp, l);
       }
       continue;
@@ -938,8 +949,10 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
         for (int e = 0; e < 4; ++e)
           st_global<f32x4>(part_out + (4 * b + e) * 256,
                            f32x4{y[b][4 * e], y[b][4 * e + 1], y[b][4 * e + 2], y[b][4 * e + 3]});
-      if (h == 0 && part == 0)
+      if (h == 0 && part == 0) {
         st_global<f32x2>(a.ws + g.stats_off + ((int64_t)place * kRows + in) * 8, f32x2{base - kUp, l});
+        if constexpr (kI8) st_global<float>(a.ws + g.units_off + ((int64_t)place * kRows + in) * 4, v_base);
+      }
     }
     if (tid == (place & 1)) {   // (which cleared it)
       // The first and the last stretch that hold a tile of the item.
@@ -960,11 +973,12 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
 // and kMany 8 and 6 leave that prompt at 25 to 26.)
 constexpr int kHelpers = 2, kMany = 16;
 
-template <int D>
+template <int D, bool I8>
 __global__ void __launch_bounds__(256) join_kernel(ChunkArgs a, ChunkGrid g) {
   constexpr int kBlocks = D / 32;
   __shared__ f32x4 sh_z[4][64];
   __shared__ f32x2 sh_st[4][64];
+  __shared__ float sh_unit[4][I8 ? 64 : 1];
   const Record in = reinterpret_cast<const Record *>(a.ws)[blockIdx.x];
   if (in.parts == 0) return;
   const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
@@ -973,20 +987,24 @@ __global__ void __launch_bounds__(256) join_kernel(ChunkArgs a, ChunkGrid g) {
   const int blocks = (in.count + kCols - 1) / kCols * kBlocks;
   const float *outs = reinterpret_cast<const float *>(a.ws + g.outs_off) + 4 * lane;
   const float *stats = reinterpret_cast<const float *>(a.ws + g.stats_off) + 2 * c;
+  const float *units = reinterpret_cast<const float *>(a.ws + g.units_off) + c;
   // Adds up to J parts first, first + step, ... of block `at`, E quads of a lane from e0 on.
-  auto add = [&](auto J_, int at, int e0, int first, int step, float &top, float &sum, auto &z) {
+  auto add = [&](auto J_, int at, int e0, int first, int step, float &top, float &sum, float &unit, auto &z) {
     constexpr int J = decltype(J_)::value, E = sizeof(z) / sizeof(z[0]);
     f32x2 st[J];
+    float un[J];
     f32x4 x[J][E];
 #pragma unroll
     for (int u = 0; u < J; ++u) {
       const int p = first + u * step;
       st[u] = f32x2{-INFINITY, 0.0f};
+      un[u] = kNoUnit;
 #pragma unroll
       for (int e = 0; e < E; ++e) x[u][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       if (p < in.parts) {
         const int64_t place = p == 0 ? in.place : 2 * (in.w + p);
         st[u] = ld_global<f32x2>(stats + (place * kRows + at / kBlocks * kCols) * 2);
+        if constexpr (I8) un[u] = ld_global<float>(units + place * kRows + at / kBlocks * kCols);
 #pragma unroll
         for (int e = 0; e < E; ++e)
           x[u][e] = ld_global<f32x4>(outs + place * kRows * D + at * 1024 + (e0 + e) * 256);
@@ -995,20 +1013,29 @@ __global__ void __launch_bounds__(256) join_kernel(ChunkArgs a, ChunkGrid g) {
     float t = top;
 #pragma unroll
     for (int u = 0; u < J; ++u) t = fmaxf(t, st[u].x);
-    const float zero = t == -INFINITY ? 0.0f : t, keep = exp2_fast(top - zero);
+    const float zero = t == -INFINITY ? 0.0f : t;
+    float keep = exp2_fast(top - zero);
     top = t;
     sum *= keep;
+    if constexpr (I8) {
+      float w = unit;
+#pragma unroll
+      for (int u = 0; u < J; ++u) w = fmaxf(w, un[u]);
+      keep *= exp2_fast(unit - w);
+      unit = w;
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e) z[e] *= keep;
 #pragma unroll
     for (int u = 0; u < J; ++u) {
-      const float f = exp2_fast(st[u].x - zero);
+      float f = exp2_fast(st[u].x - zero);
       sum += st[u].y * f;
+      if constexpr (I8) f *= exp2_fast(un[u] - unit);
 #pragma unroll
       for (int e = 0; e < E; ++e) z[e] += x[u][e] * f;
     }
   };
-  auto store = [&](int at, int e0, float top, float sum, const auto &z) {
+  auto store = [&](int at, int e0, float top, float sum, float unit, const auto &z) {
     const int group = at / kBlocks, b = at % kBlocks, at_row = group * kCols + c;
     if (at_row >= in.count) return;
     const int m = in.m0 + at_row, i = m / g.per;
@@ -1016,43 +1043,48 @@ __global__ void __launch_bounds__(256) join_kernel(ChunkArgs a, ChunkGrid g) {
     const float over = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
     for (int e = 0; e < (int)(sizeof(z) / sizeof(z[0])); ++e)
-      st_global<f32x4>(a.out + row * D + 32 * b + 8 * (e0 + e) + 4 * h, z[e] * over);
+      st_global<f32x4>(a.out + row * D + 32 * b + 8 * (e0 + e) + 4 * h, mean_of<I8>(z[e], over, unit));
     if (a.lse && b == 0 && e0 == 0 && h == 0) a.lse[row] = row_lse(top, sum);
   };
   constexpr f32x4 kZero = {0.0f, 0.0f, 0.0f, 0.0f};
   if (in.parts < kMany) {
     for (int at = 4 * helper + wave; at < blocks; at += 4 * helpers) {
-      float top = -INFINITY, sum = 0.0f;
+      float top = -INFINITY, sum = 0.0f, unit = kNoUnit;
       f32x4 z[4] = {kZero, kZero, kZero, kZero};
       for (int p = 0; p < in.parts; p += 8)
-        add(std::integral_constant<int, 8>{}, at, 0, p, 1, top, sum, z);
-      store(at, 0, top, sum, z);
+        add(std::integral_constant<int, 8>{}, at, 0, p, 1, top, sum, unit, z);
+      store(at, 0, top, sum, unit, z);
     }
     return;
   }
-  for (int unit = helper; unit < 4 * blocks; unit += helpers) {
-    const int at = unit >> 2, e = unit & 3;
-    float top = -INFINITY, sum = 0.0f;
+  for (int n = helper; n < 4 * blocks; n += helpers) {
+    const int at = n >> 2, e = n & 3;
+    float top = -INFINITY, sum = 0.0f, unit = kNoUnit;
     f32x4 z[1] = {kZero};
     for (int p = wave; p < in.parts; p += 4 * 16)
-      add(std::integral_constant<int, 16>{}, at, e, p, 4, top, sum, z);
+      add(std::integral_constant<int, 16>{}, at, e, p, 4, top, sum, unit, z);
     sh_z[wave][lane] = z[0];
     sh_st[wave][lane] = f32x2{top, sum};
+    if constexpr (I8) sh_unit[wave][lane] = unit;
     __syncthreads();
     if (wave == 0) {
       float all = -INFINITY;
 #pragma unroll
       for (int s = 0; s < 4; ++s) all = fmaxf(all, sh_st[s][lane].x);
       const float zero = all == -INFINITY ? 0.0f : all;
+      if constexpr (I8)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) unit = fmaxf(unit, sh_unit[s][lane]);
       sum = 0.0f;
       z[0] = kZero;
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const float f = exp2_fast(sh_st[s][lane].x - zero);
+        float f = exp2_fast(sh_st[s][lane].x - zero);
         sum += sh_st[s][lane].y * f;
+        if constexpr (I8) f *= exp2_fast(sh_unit[s][lane] - unit);
         z[0] += sh_z[s][lane] * f;
       }
-      store(at, e, all, sum, z);
+      store(at, e, all, sum, unit, z);
     }
     __syncthreads();
   }
@@ -1069,7 +1101,7 @@ void chunk_requests(const ChunkArgs &a, const ChunkGrid &g, hipStream_t stream) 
   else
     chunk_kernel<DT, D, false, false><<<g.groups, threads_of(D), 0, stream>>>(a, g);
   if (g.groups > 1)   // (else nothing is cut)
-    join_kernel<D><<<dim3(2 * g.groups, kHelpers), 256, 0, stream>>>(a, g);
+    join_kernel<D, DT == BITNET_KV_INT8><<<dim3(2 * g.groups, kHelpers), 256, 0, stream>>>(a, g);
 }
 
 template <int DT>
@@ -1078,6 +1110,7 @@ void chunk_type(const ChunkArgs &a, int D, hipStream_t stream) {
   ChunkGrid g;
   g.outs_off = (int64_t)p.outs;
   g.stats_off = (int64_t)p.stats;
+  g.units_off = (int64_t)p.units;
   g.groups = p.groups;
   g.per = a.q_heads / a.c.kv_heads;
   g.over_groups = 1.0 / g.groups;
