@@ -75,9 +75,9 @@ __device__ __forceinline__ void store_codes(const f32x4 (&y)[VEC], int t, int qu
     const int i = t + j * 64 * WAVES;
     if (i >= quads) continue;
     uint32_t q;
-    if (s < INFINITY)
+    if (s > 0.0f && s < INFINITY)
       q = codes_of(y[j], s);
-    else   // 127 / max overflows: as the quantization of the fp32 row has it
+    else   // 127 / max overflows, or y did: as the quantization of the fp32 row has it
       q = pack4_i8(quant_one(y[j].x, s), quant_one(y[j].y, s), quant_one(y[j].z, s),
                    quant_one(y[j].w, s));
     st_global<uint32_t>(xq + 4 * i, q);
