@@ -700,7 +700,7 @@ bitnet_status bitnet_paged_attention(const bitnet_kv_cache *cache, int32_t layer
  *   workspace: bitnet_chunk_attention_workspace_bytes(...) bytes, 256-byte
  *   aligned; what it holds before does not matter, and nothing is kept in it
  *   from one call to the next (calls that share it must not overlap in time).
- *   Two launches.
+ *   One launch, or two where items may be cut.
  */
 size_t bitnet_chunk_attention_workspace_bytes(int64_t T, int64_t R, int64_t q_heads,
                                               int64_t kv_heads, int64_t head_dim,
@@ -786,7 +786,7 @@ bitnet_status bitnet_beam_reorder(const bitnet_kv_cache *cache, int64_t B, int64
  * bitnet_add_rms_norm: h = fl32(x + residual) (residual NULL: h = x),
  *     y = fl32(h * weight / sqrt(mean_k h^2 + eps)),
  *   computed in fp64 and rounded once (off by half a unit in the last place
- *   plus 2^-50 relative); a row with a zero under the root gives zeros.
+ *   plus 2^-48 relative); a row with a zero under the root gives zeros.
  *   sum_out (optional) takes h; it may be residual or x itself where their
  *   rows are contiguous.
  * bitnet_silu_mul: y = fl32(gate * up / (1 + exp(-gate))), in the same way

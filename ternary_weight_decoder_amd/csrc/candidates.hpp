@@ -51,7 +51,8 @@ __device__ __forceinline__ double exponent(float m) {
 // The difference of two maxima's exponents, m <= n, n > -inf, and its exp2.  An fma
 // gives a rounded product's difference to an exact one; of two large maxima the
 // difference itself is exact where its exp2 is not zero.  (Selects: with a branch to
-// fp64 16 groups of 4 beams of 32,000 logits take 11.4 us, 11.2 so.)
+// fp64 32 groups of 32 beams of 40,000 logits take 66.2 us, 65.3 so; one group of 4 beams
+// of 151,936 11.4 and 11.1.)
 __device__ __forceinline__ float rise(float m, float n) {
   const float mc = m * kLog2e, nc = n * kLog2e;
   const float to_near = huge(m) ? __builtin_fmaf(m, kLog2e, -nc) : mc - nc;

@@ -38,17 +38,18 @@
 // rows: a linear function of the tile's number, so every place on the line has
 // a closed form and no list of items is made.  What an item's beginning and end
 // cost (queries as terms, the first tiles' way from memory, the joining) counts as
-// some 200 tokens.  A stretch may hold the end of an item, whole ones and the
+// 256 tokens, 160 with 256 channels.  A stretch may hold the end of an item, whole ones and the
 // beginning of another; the parts of items that are cut go to the workspace, and a
 // second launch joins them.  (Its launch takes 2 us and what it reads and writes 2
 // of a tail of 4 tokens, 6 of a prompt of 1800, near HBM's rate.)
 //
-// Measured, 12 heads over 2 of 128 channels: 1800 fp16 tokens 44 us (20 GFLOP of
-// terms' products: 18 us at a large product's rate; then 2 us of start, 3 of plan
-// and place, 6 of first tiles and queries for each of an item's parts, 8 of parts and
-// join); 16 requests of 1..256 tokens behind up to 1800 in 8 bits 63 us; 450 bf16
-// tokens behind 32,317 233 to 250 us by the card (270 GFLOP: 1.08 to 1.16 PFLOP/s, a
-// large product's rate); 4 tokens behind 253 14.5 us.
+// Measured, 12 heads over 2 of 128 channels, on the same inputs again and in turn over
+// several: 1800 fp16 tokens 44 and 46 us (20 GFLOP of terms' products: 18 us at a large
+// product's rate; then 2 us of start, 3 of plan and place, 6 of first tiles and queries
+// for each of an item's parts, 8 of parts and join); 16 requests of 1..256 tokens behind
+// up to 1800 in 8 bits 62 and 66 us; 450 bf16 tokens behind 32,317 231 to 242 us by the
+// card (270 GFLOP: 1.12 to 1.17 PFLOP/s, a large product's rate); 4 tokens behind 253
+// 14.1 to 14.6 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -379,7 +380,7 @@ chunk_kernel(ChunkArgs a, ChunkGrid g) {
   const double over_stretch = inverse(stretch);
   // Workgroups go round the eight dies in turn: neighbours on the line, which read the
   // same keys and values, to one of them (a prompt fetches 18 MB instead of 38 and takes
-  // 0.5 us less, 16 ragged requests 26 MB instead of 74).
+  // 0.5 us less, 16 ragged requests 28 MB instead of 74).
   const int w = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
   const double begin = w * stretch, stop = fmin(begin + stretch, total);
   double pos = begin;
